@@ -294,6 +294,159 @@ bi_status bi_decode_attention(const void *q, const void *k_cache, const void *v_
 size_t bi_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t Lmax);
 
 /*
+ * bi_rope -- rotary positions: y = x with the first R entries of every head turned by its token's
+ * position.  Pair number i < R/2 of head h of token t, entries (a, b) of x, becomes
+ *   (a cos w - b sin w, b cos w + a sin w) * scale,   w = positions[t] * inv_freq[i],
+ * and entries R .. D-1 are copied as they are.  `inverse` turns by -w: the transposed map, which is
+ * the gradient of the forward one.  Elementwise, so batch-invariant by construction; not an
+ * operation the pages name (the attention input of the workload's model).
+ *
+ *   x, y       device, [T, H, D] of x_dtype (bf16 or fp32), entries of a head consecutive, tokens and
+ *              heads token_stride / head_stride elements apart (any strides >= 0 for x; those of y
+ *              must keep its heads apart).  y may be x itself with the same strides.
+ *   positions  device, int32, [T], any sign.
+ *   inv_freq   device, fp64, [R/2] (bi_rope_freqs).  R even, 0 <= R <= D <= 1024.
+ *   layout     BI_ROPE_HALF: pair i is entries (i, i + R/2); BI_ROPE_INTERLEAVED: (2i, 2i + 1).
+ *   The angle is an fp64 product reduced to a fraction of a turn, so far positions keep their
+ *   digits; the rest is fp32 with one rounding to bf16.  16-byte pieces are moved where R/2, D - R,
+ *   the strides and the addresses allow it, single entries otherwise, with the same bits.
+ *   T <= 2^31 - 1, H <= 65535.
+ */
+typedef enum { BI_ROPE_HALF = 0, BI_ROPE_INTERLEAVED = 1 } bi_rope_layout;
+
+bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y, int64_t y_token_stride,
+                  int64_t y_head_stride, bi_dtype x_dtype, const int32_t *positions, const double *inv_freq,
+                  int64_t T, int64_t H, int64_t D, int64_t R, bi_rope_layout layout, float scale, int inverse,
+                  void *stream);
+
+/*
+ * bi_rope_freqs -- the inverse frequencies theta^(-2i/R), i < R/2, and the output scale of a scaled
+ * variant, in host memory (no device is touched).  kind and params:
+ *   BI_ROPE_PLAIN   none.  scale 1.
+ *   BI_ROPE_LINEAR  {factor}: every frequency / factor.  scale 1.
+ *   BI_ROPE_NTK     {factor}: theta replaced by theta * factor^(R / (R - 2)) (R > 2).  scale 1.
+ *   BI_ROPE_YARN    {factor, original length, beta_fast, beta_slow}: frequency i is blended from f (more than
+ *                   beta_fast turns within the original length) to f / factor (fewer than beta_slow) by a
+ *                   linear ramp over i between the two bounds, floor and ceiling of
+ *                   R log(length / (2 pi beta)) / (2 log theta).  scale 0.1 log(factor) + 1.
+ *   BI_ROPE_BANDED  {factor, original length, low, high}: wavelengths shorter than length / high keep f, longer than
+ *                   length / low get f / factor, between them the two are blended linearly in
+ *                   length / wavelength.  scale 1.
+ * theta > 1, factor >= 1, lengths > 0, beta_fast > beta_slow > 0, high > low > 0; otherwise BI_ERR_INVALID_ARG.
+ */
+typedef enum {
+    BI_ROPE_PLAIN = 0,
+    BI_ROPE_LINEAR = 1,
+    BI_ROPE_NTK = 2,
+    BI_ROPE_YARN = 3,
+    BI_ROPE_BANDED = 4
+} bi_rope_kind;
+
+bi_status bi_rope_freqs(int64_t R, double theta, bi_rope_kind kind, const double *params, int64_t n_params,
+                        double *inv_freq, double *scale);
+
+/*
+ * A paged key/value cache: `pages` pages of page_size tokens, bf16.  Entry d of head h of row r of page
+ * g is k[g * page_stride + r * token_stride + h * head_stride + d] (strides in elements, the same for
+ * v), so [pages, page_size, heads, D], [pages, heads, page_size, D] and keys beside values in one
+ * buffer are all described.  A sequence's tokens p = 0, 1, ... sit in row p % page_size of page
+ * block_table[b][p / page_size].  k and v 16-byte aligned, strides multiples of 8.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t pages, page_size, heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+} bi_paged_cache;
+
+/*
+ * bi_paged_append -- write new tokens' keys and values into a paged cache, the keys turned as bi_rope
+ * turns them, and optionally turn the same tokens' queries.  Elementwise, batch-invariant by
+ * construction; not an operation the pages name (the step before bi_paged_decode_attention).
+ *
+ *   k, v        device, bf16, [T, heads, D], token and head strides as in bi_rope.
+ *   q, q_out    device, bf16, [T, Hq, D], or both NULL; q_out may be q with the same strides.
+ *   cu_new      device, int32, [B+1], ascending: the new tokens of sequence b are cu_new[b] .. cu_new[b+1]-1.
+ *               NULL: T = B, one each.
+ *   seq_lens    device, int32, [B]: tokens of each sequence with the new ones, which come last: token t
+ *               of sequence b takes place seq_lens[b] - (cu_new[b+1] - t).
+ *   block_table device, int32, [B, max_pages], rows table_stride elements apart.
+ *   positions   device, int32, [T]: what turns each token, or NULL: its place.
+ *   inv_freq    device, fp64, [R/2], as in bi_rope; R = 0: nothing is turned (NULL).
+ * Tokens behind cu_new[B] (or before cu_new[0]) and those of a sequence with seq_lens[b] = 0 are skipped:
+ * nothing of theirs is read back or written.  A place that is negative or past the table, or a page
+ * outside 0 .. pages-1, records BI_ERR_INVALID_ARG in the device status word and skips the token.
+ * Two tokens must not share a place: pages that receive tokens belong to one sequence.
+ * D <= 1024, heads and Hq <= 65535, T, B < 2^31, pages and page_size <= 2^31 - 1.
+ * Pieces as in bi_rope; k, v, q need no alignment beyond their type's.
+ */
+bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, void *q_out, int64_t q_out_token_stride,
+                          int64_t q_out_head_stride, int64_t Hq, const bi_paged_cache *cache,
+                          const int32_t *block_table, int64_t table_stride, int64_t max_pages,
+                          const int32_t *seq_lens, const int32_t *cu_new, const int32_t *positions,
+                          const double *inv_freq, int64_t R, bi_rope_layout layout, float scale, int64_t T,
+                          int64_t B, void *stream);
+
+/*
+ * bi_paged_decode_attention -- bi_decode_attention over a paged cache: for each sequence b and query head
+ * h (reading kv head h / (Hq / heads)), out[b,h,:] = sum_t p_t v_t with p = softmax(scale * q[b,h,:] . k_t)
+ * over the sequence's t < seq_lens[b].  A sequence of length 0 (an empty place of a padded batch) gets zeros.
+ * Passage: as bi_decode_attention.
+ *
+ * Batch invariance: a sequence is cut into splits of 256 tokens and tiles of 32, cuts fixed by the token's
+ * own place; a tile's scores are fp32 dot products, its weights relative to its own maximum; tiles fold in
+ * order within a split, and splits in a tree fixed by their number.  A sequence's output does not depend on
+ * the others, on where its pages lie, on the page size or on max_len.
+ *
+ *   q        device, bf16, [B, Hq, D], heads consecutive, sequences q_stride elements apart (a multiple of 8).
+ *   out      device, bf16, [B, Hq, D] contiguous (one rounding).
+ *   seq_lens device, int32, [B], each in 0 .. max_len.  A value outside is clamped and BI_ERR_INVALID_ARG
+ *            recorded in the device status word.
+ *   block_table as in bi_paged_append; only the entries of a sequence's own tokens are read.  A page outside
+ *            0 .. pages-1 records BI_ERR_INVALID_ARG and its tokens count with keys and values of zero.
+ *   max_len  what the host knows of the longest sequence, 1 .. max_pages * page_size.
+ *   D must be 64 or 128 and Hq / heads 1 .. 16, any page_size >= 1 (else BI_ERR_UNSUPPORTED; pages of fewer
+ *   than 8 tokens, or of an odd number, take more and smaller copies); B, Hq <= 65535 and
+ *   min(B, 2048) * heads * ceil(max_len / 256) < 2^31.
+ *   scratch  caller-owned device memory, 16-byte aligned, bi_paged_decode_attention_scratch_bytes bytes;
+ *            overwritten (two launches on `stream` per 2048 sequences; one when max_len <= 256), so
+ *            overlapping calls need separate scratch.
+ *   q, out 16-byte aligned.
+ */
+bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_paged_cache *cache,
+                                    const int32_t *block_table, int64_t table_stride, int64_t max_pages,
+                                    const int32_t *seq_lens, void *out, int64_t B, int64_t Hq, int64_t max_len,
+                                    float scale, void *scratch, size_t scratch_bytes, void *stream);
+
+/* Bytes of scratch bi_paged_decode_attention needs (0 if any size is <= 0 or max_len <= 256). */
+size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len);
+
+/*
+ * bi_token_logprobs -- what sampling and scoring keep of bi_log_softmax, without writing [M, V] values.
+ * Per row, with z = scale * x (scale = 1 / temperature) and y = z - logsumexp(z):
+ *   logprobs_i = y[tokens_i],  entropy_i = -sum_j exp(y_j) y_j (0 where exp(y_j) = 0),
+ *   logsumexp_i, and the top_k largest y_j with their tokens, in descending order, equal logits in
+ *   ascending token order.
+ * Passage: as bi_log_softmax.
+ *
+ *   x        device, [M, V] of x_dtype (bf16 or fp32), rows ldx >= V elements apart.
+ *   tokens   device, int32, [M].  A negative one is not scored (logprob 0); one >= V gives NaN and records
+ *            BI_ERR_INVALID_ARG in the device status word.
+ *   logprobs, entropy, logsumexp  device, fp32, [M]; each may be NULL (tokens may be when logprobs is).
+ *   top_logprobs, top_tokens  device, fp32 / int32, [M, top_k]; 0 <= top_k <= min(32, V).
+ *   -inf logits are masked entries.  A row of only -inf has logsumexp -inf and NaN elsewhere; +inf or NaN
+ *   in a row makes its values NaN.  NaN logits rank below all others.
+ *   1 <= V <= 262144.  scale > 0, finite.  Rows of any alignment; 16-byte aligned rows are read faster.
+ * Batch invariance: a row is cut into pieces of 16384 (bf16) or 8192 (fp32) elements, each reduced in one
+ * fixed order by one block and folded in one fixed tree.  How many blocks share a row's pieces depends on
+ * M and changes no bit.
+ */
+bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const int32_t *tokens, float scale,
+                            int64_t top_k, float *logprobs, float *entropy, float *logsumexp, float *top_logprobs,
+                            int32_t *top_tokens, int64_t M, int64_t V, void *stream);
+
+/*
  * bi_get_device_status -- synchronise `stream`, then read and clear the current
  * device's status word.  *out receives BI_OK or the first error a kernel recorded
  * since the last read (BI_ERR_TIMEOUT for a bounded wait that ran out).

@@ -7,6 +7,7 @@ libbi.so is loaded on the first call into ``binding``.
 """
 from .binding import (  # noqa: F401
     BiError,
+    TokenLogprobs,
     bi_addmm,
     bi_decode_attention,
     bi_decode_attention_scratch_bytes,
@@ -18,9 +19,15 @@ from .binding import (  # noqa: F401
     bi_matmul,
     bi_matmul_silu_mul,
     bi_mean,
+    bi_paged_append,
+    bi_paged_decode_attention,
+    bi_paged_decode_attention_scratch_bytes,
     bi_rmsnorm,
+    bi_rope,
+    bi_rope_freqs,
     bi_selftest_wait_timeout,
     bi_silu_mul,
+    bi_token_logprobs,
     bi_version,
     load,
 )

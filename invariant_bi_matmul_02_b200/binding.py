@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -20,9 +21,23 @@ LIB_PATH = os.path.join(_HERE, "libbi.so")
 BI_OK, BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED, BI_ERR_ALIGNMENT, BI_ERR_CUDA, BI_ERR_TIMEOUT = range(6)
 BI_BF16, BI_F32 = 0, 1
 BI_B_KN, BI_B_NK = 0, 1
+BI_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+# Kinds of bi_rope_freqs and the parameters each takes, in order.
+BI_ROPE_KINDS = {"plain": (0, ()), "linear": (1, ("factor",)), "ntk": (2, ("factor",)),
+                 "yarn": (3, ("factor", "original_length", "beta_fast", "beta_slow")),
+                 "banded": (4, ("factor", "original_length", "low", "high"))}
 
-# Every entry point declared in include/bi.h, with its ctypes signature.
 _i64, _p, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
+
+
+class PagedCache(ctypes.Structure):
+    """bi_paged_cache of include/bi.h."""
+    _fields_ = [("k", _p), ("v", _p)] + [(n, _i64) for n in ("pages", "page_size", "heads", "head_dim", "page_stride",
+                                                            "token_stride", "head_stride")]
+
+
+_pf64 = ctypes.POINTER(ctypes.c_double)
+# Every entry point declared in include/bi.h, with its ctypes signature.
 SIGNATURES = {
     "bi_matmul": (ctypes.c_int, [_p, _i64, _p, _i64, ctypes.c_int, _p, _i64, ctypes.c_int,
                                  _i64, _i64, _i64, _p]),
@@ -41,6 +56,17 @@ SIGNATURES = {
     "bi_decode_attention": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, ctypes.c_float,
                                            _p, ctypes.c_size_t, _p]),
     "bi_decode_attention_scratch_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
+    "bi_rope": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, ctypes.c_int, _p, _p, _i64, _i64, _i64, _i64,
+                               ctypes.c_int, ctypes.c_float, ctypes.c_int, _p]),
+    "bi_rope_freqs": (ctypes.c_int, [_i64, ctypes.c_double, ctypes.c_int, _pf64, _i64, _pf64, _pf64]),
+    "bi_paged_append": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64,
+                                       ctypes.POINTER(PagedCache), _p, _i64, _i64, _p, _p, _p, _p, _i64,
+                                       ctypes.c_int, ctypes.c_float, _i64, _i64, _p]),
+    "bi_paged_decode_attention": (ctypes.c_int, [_p, _i64, ctypes.POINTER(PagedCache), _p, _i64, _i64, _p, _p, _i64,
+                                                 _i64, _i64, ctypes.c_float, _p, ctypes.c_size_t, _p]),
+    "bi_paged_decode_attention_scratch_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i64]),
+    "bi_token_logprobs": (ctypes.c_int, [_p, _i64, ctypes.c_int, _p, ctypes.c_float, _i64, _p, _p, _p, _p, _p, _i64,
+                                         _i64, _p]),
     "bi_get_device_status": (ctypes.c_int, [_p, ctypes.POINTER(_i32)]),
     "bi_selftest_wait_timeout": (ctypes.c_int, [_i64, _p]),
     "bi_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -386,6 +412,220 @@ def bi_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
         B, Hq, Hkv, D, Lmax, float(scale), scratch.data_ptr(), nbytes, _stream(stream)))
     return out
+
+
+def _heads(t: torch.Tensor, name: str, dtypes, cur: int | None) -> int:
+    """Check a [T, H, D] tensor whose heads' entries are consecutive; returns the current device."""
+    cur = _need_cuda(t, name, dtypes, cur)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D]")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: a head's entries must be contiguous")
+    return cur
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int | None, cur: int) -> int:
+    """Check a contiguous vector (of n entries, if n is given); returns its address."""
+    _need_cuda(t, name, (dtype,), cur)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a vector" + ("" if n is None else f" of {n}"))
+    _contig(t, name)
+    return t.data_ptr()
+
+
+def _rope_layout(layout: str) -> int:
+    if layout not in BI_ROPE_LAYOUTS:
+        raise ValueError("layout must be 'half' (pairs i, i + R/2) or 'interleaved' (pairs 2i, 2i + 1)")
+    return BI_ROPE_LAYOUTS[layout]
+
+
+def bi_rope_freqs(rotary_dim: int, theta: float = 10000.0, kind: str = "plain", device=None,
+                  **params: float) -> tuple[torch.Tensor, float]:
+    """(inv_freq, scale): the fp64 inverse frequencies [rotary_dim / 2] of a rotary embedding on
+    `device` (default: the current CUDA device) and its output scale.  kind: 'plain', 'linear' (factor), 'ntk'
+    (factor), 'yarn' (factor, original_length, beta_fast=32, beta_slow=1) or 'banded' (factor, original_length, low,
+    high)."""
+    if kind not in BI_ROPE_KINDS:
+        raise ValueError(f"kind must be one of {tuple(BI_ROPE_KINDS)}")
+    code, names = BI_ROPE_KINDS[kind]
+    if kind == "yarn":
+        params = {"beta_fast": 32.0, "beta_slow": 1.0, **params}
+    if set(params) != set(names):
+        raise ValueError(f"kind '{kind}' takes {names}, got {tuple(params)}")
+    n = max(int(rotary_dim) // 2, 0)
+    out, scale = (ctypes.c_double * max(n, 1))(), ctypes.c_double(1.0)
+    given = (ctypes.c_double * max(len(names), 1))(*[float(params[k]) for k in names])
+    _check("bi_rope_freqs", load().bi_rope_freqs(int(rotary_dim), float(theta), code, given, len(names), out,
+                                                 ctypes.byref(scale)))
+    if device is None:
+        device = torch.device("cuda", _current_device())
+    return torch.tensor(list(out)[:n], dtype=torch.float64, device=device), float(scale.value)
+
+
+def bi_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: str = "half",
+            scale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x [T, H, D] (bf16 or fp32, token and head strides free) with the first 2 * len(inv_freq) entries of
+    every head turned by positions [T] (int32); `inverse` turns back (the gradient's map).  out may be x."""
+    cur = _heads(x, "x", (torch.bfloat16, torch.float32), None)
+    T, H, D = x.shape
+    pos = _vector(positions, "positions", torch.int32, T, cur)
+    freq = _vector(inv_freq, "inv_freq", torch.float64, None, cur)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    _heads(out, "out", (x.dtype,), cur)
+    if tuple(out.shape) != (T, H, D):
+        raise ValueError("out must be [T, H, D]")
+    _check("bi_rope", load().bi_rope(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
+                                     out.stride(1), _DT[x.dtype], pos, freq, T, H, D, 2 * inv_freq.shape[0],
+                                     _rope_layout(layout), float(scale), 1 if inverse else 0, _stream(stream, cur)))
+    return out
+
+
+def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, cur: int) -> PagedCache:
+    """The cache description of two [pages, page_size, heads, D] tensors with the same strides."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need_cuda(t, n, (torch.bfloat16,), cur)
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be [pages, page_size, heads, D] (a transposed view for pages laid out head first)")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{n}: a head's entries must be contiguous")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    pages, page_size, heads, dim = k_cache.shape
+    s = k_cache.stride()
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, heads, dim, s[0], s[1], s[2])
+
+
+def _block_table(t: torch.Tensor, B: int, cur: int):
+    """Check a [B, max_pages] int32 table with contiguous rows: its address, row stride and width."""
+    _need_cuda(t, "block_table", (torch.int32,), cur)
+    if t.dim() != 2 or t.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    return t.data_ptr(), _ld(t, "block_table"), t.shape[1]
+
+
+def bi_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
+                    inv_freq: torch.Tensor | None = None, layout: str = "half", scale: float = 1.0,
+                    q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                    positions: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Write new tokens' k, v [T, heads, D] into the paged caches [pages, page_size, heads, D] (k turned as by
+    bi_rope when inv_freq is given) and return the turned q [T, Hq, D], if q is given.  seq_lens [B] counts the
+    new tokens, which come last; cu_new [B+1] delimits them (None: one per sequence); positions [T] replaces
+    the places that turn them.  q_out may be q.  Tokens that are skipped (behind cu_new[B], or of a sequence of
+    length 0) leave their q_out rows as they were."""
+    bf16 = (torch.bfloat16,)
+    cur = _heads(k, "k", bf16, None)
+    _heads(v, "v", bf16, cur)
+    cache = _paged_cache(k_cache, v_cache, cur)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, cache.heads, cache.head_dim) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, heads, D] of the cache's heads and D")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    lens = _vector(seq_lens, "seq_lens", torch.int32, None, cur)
+    table, table_stride, max_pages = _block_table(block_table, B, cur)
+    if cu_new is None and T != B:
+        raise ValueError("without cu_new every sequence has one new token: k must have B tokens")
+    cu = None if cu_new is None else _vector(cu_new, "cu_new", torch.int32, B + 1, cur)
+    pos = None if positions is None else _vector(positions, "positions", torch.int32, T, cur)
+    freq, R = None, 0
+    if inv_freq is not None:
+        freq, R = _vector(inv_freq, "inv_freq", torch.float64, None, cur), 2 * inv_freq.shape[0]
+    qs, os, Hq = (None, 0, 0), (None, 0, 0), 0
+    if q is not None:
+        _heads(q, "q", bf16, cur)
+        Hq = q.shape[1]
+        if tuple(q.shape) != (T, Hq, cache.head_dim):
+            raise ValueError("q must be [T, Hq, D]")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.head_dim), dtype=q.dtype, device=q.device)
+        _heads(q_out, "q_out", bf16, cur)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be [T, Hq, D]")
+        if Hq > 0:
+            qs, os = (q.data_ptr(), q.stride(0), q.stride(1)), (q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check("bi_paged_append", load().bi_paged_append(
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), *qs, *os, Hq,
+        ctypes.byref(cache), table, table_stride, max_pages, lens, cu, pos, freq, R, _rope_layout(layout),
+        float(scale), T, B, _stream(stream, cur)))
+    return q_out
+
+
+def bi_paged_decode_attention_scratch_bytes(B: int, Hq: int, D: int, max_len: int) -> int:
+    return int(load().bi_paged_decode_attention_scratch_bytes(int(B), int(Hq), int(D), int(max_len)))
+
+
+def bi_paged_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int | None = None,
+                              scale: float | None = None, scratch: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One decode step over a paged cache: q [B, Hq, D] (rows may be strided), caches [pages, page_size, heads, D],
+    block_table [B, max_pages] and seq_lens [B] int32.  max_len: the longest sequence as the host knows it (default:
+    all the table can name; a tighter bound needs less scratch)."""
+    cur = _heads(q, "q", (torch.bfloat16,), None)
+    cache = _paged_cache(k_cache, v_cache, cur)
+    B, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError("q's head size differs from the cache's")
+    if Hq > 1 and q.stride(1) != D:
+        raise ValueError("q: a token's heads must be contiguous")
+    lens = _vector(seq_lens, "seq_lens", torch.int32, B, cur)
+    table, table_stride, max_pages = _block_table(block_table, B, cur)
+    if max_len is None:
+        max_len = max_pages * cache.page_size
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    _need_cuda(out, "out", (torch.bfloat16,), cur)
+    _contig(out, "out")
+    if tuple(out.shape) != (B, Hq, D):
+        raise ValueError("out must be [B, Hq, D]")
+    if scratch is None:
+        scratch = torch.empty(max(bi_paged_decode_attention_scratch_bytes(B, Hq, D, max_len), 16), dtype=torch.uint8,
+                              device=q.device)
+    if not scratch.is_cuda:
+        raise ValueError("scratch must be device memory")
+    _same_device(scratch.get_device(), "scratch", cur)
+    _contig(scratch, "scratch")
+    nbytes = scratch.numel() * scratch.element_size()
+    _check("bi_paged_decode_attention", load().bi_paged_decode_attention(
+        q.data_ptr(), q.stride(0), ctypes.byref(cache), table, table_stride, max_pages, lens, out.data_ptr(), B, Hq,
+        int(max_len), float(scale), scratch.data_ptr(), nbytes, _stream(stream, cur)))
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    """What bi_token_logprobs returns; top_logprobs and top_tokens are [M, 0] when top_k is 0."""
+    logprobs: torch.Tensor | None
+    entropy: torch.Tensor
+    logsumexp: torch.Tensor
+    top_logprobs: torch.Tensor
+    top_tokens: torch.Tensor
+
+
+def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
+                      stream=None) -> TokenLogprobs:
+    """Per row of logits [M, V] (fp32 or bf16, rows may be strided) times `scale` (1 / temperature): the
+    log-probability of tokens [M] (int32; negative: not scored, 0), the entropy, the logsumexp and the top_k best
+    log-probabilities with their tokens."""
+    cur = _need_cuda(logits, "logits", (torch.float32, torch.bfloat16))
+    ld = _ld(logits, "logits")
+    M, V = logits.shape
+    top_k = int(top_k)
+    if not 0 <= top_k <= V:
+        raise ValueError("top_k must be in 0 .. V")
+    tok = None if tokens is None else _vector(tokens, "tokens", torch.int32, M, cur)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    r = TokenLogprobs(None if tokens is None else torch.empty(M, **f32), torch.empty(M, **f32), torch.empty(M, **f32),
+                      torch.empty((M, top_k), **f32), torch.empty((M, top_k), dtype=torch.int32, device=logits.device))
+    _check("bi_token_logprobs", load().bi_token_logprobs(
+        logits.data_ptr(), ld, _DT[logits.dtype], tok, float(scale), top_k,
+        None if tokens is None else r.logprobs.data_ptr(), r.entropy.data_ptr(), r.logsumexp.data_ptr(),
+        r.top_logprobs.data_ptr(), r.top_tokens.data_ptr(), M, V, _stream(stream, cur)))
+    return r
 
 
 def bi_get_device_status(stream=None) -> int:

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -18,8 +19,11 @@
 #include "gemm.cuh"
 #include "attention.cuh"
 #include "gemm_pair.cuh"
+#include "paged_attention.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 #include "rowops.cuh"
+#include "token_logprobs.cuh"
 
 // Per-device status word: 0, or the first error a kernel recorded (BI_ERR_TIMEOUT).
 __device__ int32_t g_bi_status = 0;
@@ -55,6 +59,34 @@ bi_status attn_smem_opt_in()
                           reinterpret_cast<const void *>(bi::decode_attention_split_kernel<8, D>)};
     for (const void *fn : fns)
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bi::kAttnSmem) != cudaSuccess)
+            return BI_ERR_CUDA;
+    return BI_OK;
+}
+
+// Opt the paged decode-attention kernels of head size D and the token log-probability kernels into theirs.
+template <int D>
+bi_status paged_smem_opt_in()
+{
+    const void *fns[2] = {reinterpret_cast<const void *>(bi::paged_attention_split_kernel<D, 1>),
+                          reinterpret_cast<const void *>(bi::paged_attention_split_kernel<D, 2>)};
+    for (const void *fn : fns)
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bi::PgShape<D>::kSmem) != cudaSuccess)
+            return BI_ERR_CUDA;
+    return BI_OK;
+}
+
+// Shared memory of a token_logprobs block that takes `pieces` pieces.
+inline size_t token_logprobs_smem(int64_t pieces, int64_t top) { return top > 0 ? (size_t)pieces * bi::kTlThreads * 4 : 0; }
+
+bi_status token_logprobs_smem_opt_in()
+{
+    const void *fns[4] = {reinterpret_cast<const void *>(bi::token_logprobs_kernel<true, true>),
+                          reinterpret_cast<const void *>(bi::token_logprobs_kernel<true, false>),
+                          reinterpret_cast<const void *>(bi::token_logprobs_kernel<false, true>),
+                          reinterpret_cast<const void *>(bi::token_logprobs_kernel<false, false>)};
+    for (const void *fn : fns)
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)token_logprobs_smem(bi::kTlMaxPieces, 1)) != cudaSuccess)
             return BI_ERR_CUDA;
     return BI_OK;
 }
@@ -101,6 +133,8 @@ bi_status device_state(DeviceState **out)
             pair_clusters<bi::MidTile>(d.sms, &d.gemm_clusters_mid) != BI_OK)
             return BI_ERR_CUDA;
         if (attn_smem_opt_in<64>() != BI_OK || attn_smem_opt_in<128>() != BI_OK) return BI_ERR_CUDA;
+        if (paged_smem_opt_in<64>() != BI_OK || paged_smem_opt_in<128>() != BI_OK) return BI_ERR_CUDA;
+        if (token_logprobs_smem_opt_in() != BI_OK) return BI_ERR_CUDA;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.mean_rows_blocks_per_sm, bi::mean_rows_kernel,
                                                           bi::kMeanRowsThreads, 0) !=
                 cudaSuccess ||
@@ -230,6 +264,29 @@ bi_status encode_kv_map(CUtensorMap *map, const void *base, uint64_t D, uint64_t
     return r == CUDA_SUCCESS ? BI_OK : BI_ERR_CUDA;
 }
 
+// 4-D bf16 tensor map over one side of a paged cache: entries innermost, pages outermost, heads and rows
+// of a page between them by ascending stride (heads_inner: heads first); box 64 entries x `box` rows of
+// one head of one page, 128-byte swizzle, zero fill outside.  A dimension of one entry is never
+// stepped over, so its stride is replaced by one the encoder accepts.
+bi_status encode_page_map(CUtensorMap *map, const void *base, const bi_paged_cache &c, bool heads_inner, uint32_t box)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return BI_ERR_CUDA;
+    const uint64_t D = (uint64_t)c.head_dim;
+    const uint64_t head = c.heads > 1 ? (uint64_t)c.head_stride : D;
+    const uint64_t token = c.page_size > 1 ? (uint64_t)c.token_stride : D;
+    const uint64_t page = c.pages > 1 ? (uint64_t)c.page_stride : D;
+    const uint64_t heads = (uint64_t)c.heads, rows = (uint64_t)c.page_size;
+    const cuuint64_t dims[4] = {D, heads_inner ? heads : rows, heads_inner ? rows : heads, (uint64_t)c.pages};
+    const cuuint64_t strides[3] = {2 * (heads_inner ? head : token), 2 * (heads_inner ? token : head), 2 * page};
+    const cuuint32_t boxes[4] = {64, heads_inner ? 1 : box, heads_inner ? box : 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, boxes, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BI_OK : BI_ERR_CUDA;
+}
+
 // Launch `kernel` on `s` and report the launch's own result.  cudaLaunchKernelEx returns the
 // error of this launch, so a failure left behind by some other library's launch on this thread
 // is neither reported as ours nor cleared.
@@ -261,6 +318,28 @@ bi_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+}
+
+// launch_pdl with clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+bi_status launch_pdl_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                              cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attrs[2]{};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
 }
 
@@ -434,6 +513,68 @@ bi_status split_launches(bool bf16, dim3 grid, cudaStream_t s, const uint8_t *xb
                          static_cast<const float2 *>(part), y, V)
                 : launch(bi::log_softmax_split_write_kernel<false>, grid, dim3(bi::kSplitThreads), 0, s, xb,
                          static_cast<const float2 *>(part), y, V);
+}
+
+// Whether heads of `n` strided [.., heads, D] tensors can be moved in 16-byte pieces of W elements.
+inline bool rope_pieces(int64_t W, int64_t D, int64_t R) { return (R / 2) % W == 0 && (D - R) % W == 0; }
+inline bool strided_pieces(int64_t W, const void *p, int64_t s0, int64_t s1)
+{
+    return aligned16(p) && s0 % W == 0 && s1 % W == 0;
+}
+
+// Tokens per block of the rotation kernels: a few where that still leaves every SM several blocks (the
+// angles' latency is then shared), one otherwise.
+inline int rope_tokens(int64_t T, int sms) { return T >= (int64_t)4 * bi::kRopeTokens * sms ? bi::kRopeTokens : 1; }
+
+template <typename E, int W>
+bi_status launch_rope(const bi::RopeParams &p, bool half, int sms, cudaStream_t s)
+{
+    const int tokens = rope_tokens(p.T, sms);
+    const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(bi::kRopeThreads);
+    const size_t smem = (size_t)tokens * (p.R / 2) * sizeof(float2);
+    return half ? launch_pdl(bi::rope_kernel<E, W, true>, grid, block, smem, s, p, tokens)
+                : launch_pdl(bi::rope_kernel<E, W, false>, grid, block, smem, s, p, tokens);
+}
+
+template <int W>
+bi_status launch_append(const bi::AppendParams &p, bool half, int sms, cudaStream_t s)
+{
+    const int tokens = rope_tokens(p.T, sms);
+    const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(bi::kRopeThreads);
+    const size_t smem = (size_t)tokens * (p.R / 2) * sizeof(float2);
+    return half ? launch_pdl(bi::paged_append_kernel<W, true>, grid, block, smem, s, p, tokens)
+                : launch_pdl(bi::paged_append_kernel<W, false>, grid, block, smem, s, p, tokens);
+}
+
+// A cache description that the paged entry points take.
+bi_status check_cache(const bi_paged_cache *c)
+{
+    if (!c || !c->k || !c->v) return BI_ERR_INVALID_ARG;
+    if (c->pages <= 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0) return BI_ERR_INVALID_ARG;
+    if (c->pages > kI32Max || c->page_size > kI32Max || c->heads > 65535 || c->head_dim > bi::kRopeMaxDim)
+        return BI_ERR_UNSUPPORTED;
+    const int64_t D = c->head_dim, limit = int64_t(1) << 39;  // 2^40 bytes: a tensor map's largest stride
+    if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0) return BI_ERR_INVALID_ARG;
+    if ((c->pages > 1 && c->page_stride < D) || (c->page_size > 1 && c->token_stride < D) ||
+        (c->heads > 1 && c->head_stride < D))
+        return BI_ERR_INVALID_ARG;
+    if (c->page_stride >= limit || c->token_stride >= limit || c->head_stride >= limit) return BI_ERR_UNSUPPORTED;
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->pages > 1 && c->page_stride % 8) ||
+        (c->page_size > 1 && c->token_stride % 8) || (c->heads > 1 && c->head_stride % 8))
+        return BI_ERR_ALIGNMENT;
+    return BI_OK;
+}
+
+template <int D, int NT>
+bi_status launch_paged(dim3 grid, cudaStream_t s, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                       const bi::PgParams &p)
+{
+    const bi_status st = launch_pdl(bi::paged_attention_split_kernel<D, NT>, grid, dim3(bi::kPgThreads),
+                                    (size_t)bi::PgShape<D>::kSmem, s, tm_k, tm_v, p);
+    if (st != BI_OK || p.S == 1) return st;  // one split per sequence: launch 1 wrote out
+    return launch_pdl(bi::paged_attention_combine_kernel<D>, dim3((unsigned)p.Hq, (unsigned)p.B),
+                      dim3(bi::kPgCombineThreads), 0, s, static_cast<const float2 *>(p.part_ml),
+                      static_cast<const float *>(p.part_o), p.lens, p.out, (int)p.Hq, (int)p.S, (int)p.max_len);
 }
 
 inline unsigned elementwise_blocks(int64_t work, int sms)
@@ -750,6 +891,305 @@ bi_status bi_silu_mul(const void *gu, void *h, int64_t M, int64_t F, void *strea
                   static_cast<const __nv_bfloat16 *>(gu), static_cast<__nv_bfloat16 *>(h), M, F);
 }
 
+bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y, int64_t y_token_stride,
+                  int64_t y_head_stride, bi_dtype x_dtype, const int32_t *positions, const double *inv_freq,
+                  int64_t T, int64_t H, int64_t D, int64_t R, bi_rope_layout layout, float scale, int inverse,
+                  void *stream)
+{
+    if (T < 0 || H < 0 || D <= 0 || R < 0 || R > D || R % 2 != 0) return BI_ERR_INVALID_ARG;
+    if (x_dtype != BI_BF16 && x_dtype != BI_F32) return BI_ERR_INVALID_ARG;
+    if (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) return BI_ERR_INVALID_ARG;
+    if (T > kI32Max || H > 65535 || D > bi::kRopeMaxDim) return BI_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return BI_OK;
+    if (!x || !y || (R > 0 && (!positions || !inv_freq))) return BI_ERR_INVALID_ARG;
+    if (x_token_stride < 0 || x_head_stride < 0 || (T > 1 && y_token_stride < D) || (H > 1 && y_head_stride < D) ||
+        y_token_stride < 0 || y_head_stride < 0)
+        return BI_ERR_INVALID_ARG;
+    if (x == y && ((T > 1 && x_token_stride != y_token_stride) || (H > 1 && x_head_stride != y_head_stride)))
+        return BI_ERR_INVALID_ARG;
+    const bool bf16 = x_dtype == BI_BF16;
+    const uintptr_t type_mask = bf16 ? 1 : 3;
+    if ((reinterpret_cast<uintptr_t>(x) & type_mask) || (reinterpret_cast<uintptr_t>(y) & type_mask) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+        return BI_ERR_ALIGNMENT;
+    DeviceState *dev = nullptr;
+    bi_status st = device_state(&dev);
+    if (st != BI_OK) return st;
+    // Strides of dimensions of one entry are never used.
+    const int64_t xt = T > 1 ? x_token_stride : 0, xh = H > 1 ? x_head_stride : 0;
+    const int64_t yt = T > 1 ? y_token_stride : 0, yh = H > 1 ? y_head_stride : 0;
+    bi::RopeParams p{};
+    p.x = x;
+    p.y = y;
+    p.x_token = xt;
+    p.x_head = xh;
+    p.y_token = yt;
+    p.y_head = yh;
+    p.pos = positions;
+    p.inv_freq = inv_freq;
+    p.T = T;
+    p.H = (int32_t)H;
+    p.D = (int32_t)D;
+    p.R = (int32_t)R;
+    p.scale = scale;
+    p.inverse = inverse ? 1 : 0;
+    const int64_t W = bf16 ? 8 : 4;
+    const bool pieces = rope_pieces(W, D, R) && strided_pieces(W, x, xt, xh) && strided_pieces(W, y, yt, yh);
+    const bool half = layout == BI_ROPE_HALF;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (bf16)
+        return pieces ? launch_rope<__nv_bfloat16, 8>(p, half, dev->sms, s) : launch_rope<__nv_bfloat16, 1>(p, half, dev->sms, s);
+    return pieces ? launch_rope<float, 4>(p, half, dev->sms, s) : launch_rope<float, 1>(p, half, dev->sms, s);
+}
+
+bi_status bi_rope_freqs(int64_t R, double theta, bi_rope_kind kind, const double *params, int64_t n_params,
+                        double *inv_freq, double *scale)
+{
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    if (R < 0 || R % 2 != 0 || R > bi::kRopeMaxDim || !(theta > 1.0) || !std::isfinite(theta)) return BI_ERR_INVALID_ARG;
+    const int need = kind == BI_ROPE_PLAIN ? 0 : kind == BI_ROPE_LINEAR || kind == BI_ROPE_NTK ? 1 : 4;
+    if (kind < BI_ROPE_PLAIN || kind > BI_ROPE_BANDED || n_params != need || (need > 0 && !params)) return BI_ERR_INVALID_ARG;
+    if (R > 0 && !inv_freq) return BI_ERR_INVALID_ARG;
+    for (int i = 0; i < need; ++i)
+        if (!std::isfinite(params[i]) || !(params[i] > 0.0)) return BI_ERR_INVALID_ARG;
+    const double factor = need > 0 ? params[0] : 1.0;
+    if (factor < 1.0) return BI_ERR_INVALID_ARG;
+    if (kind == BI_ROPE_NTK && R == 2) return BI_ERR_INVALID_ARG;
+    if (need == 4 && !(kind == BI_ROPE_YARN ? params[2] > params[3] : params[3] > params[2])) return BI_ERR_INVALID_ARG;
+    if (kind == BI_ROPE_NTK) theta *= std::pow(factor, (double)R / (double)(R - 2));
+    double low = 0.0, high = 0.0;
+    if (kind == BI_ROPE_YARN) {
+        // The pair that makes `turns` turns within the original length.
+        auto pair_of = [&](double turns) { return R * std::log(params[1] / (turns * kTwoPi)) / (2.0 * std::log(theta)); };
+        low = std::fmax(std::floor(pair_of(params[2])), 0.0);
+        high = std::fmin(std::ceil(pair_of(params[3])), (double)(R - 1));
+        if (low == high) high += 0.001;
+    }
+    for (int64_t i = 0; i < R / 2; ++i) {
+        const double f = std::pow(theta, -2.0 * (double)i / (double)R);
+        double g = f;
+        if (kind == BI_ROPE_LINEAR) {
+            g = f / factor;
+        } else if (kind == BI_ROPE_YARN) {
+            const double ramp = std::fmin(std::fmax(((double)i - low) / (high - low), 0.0), 1.0);
+            g = f / factor * ramp + f * (1.0 - ramp);
+        } else if (kind == BI_ROPE_BANDED) {
+            const double turns = params[1] * f / kTwoPi;  // within the original length
+            const double keep = std::fmin(std::fmax((turns - params[2]) / (params[3] - params[2]), 0.0), 1.0);
+            g = (1.0 - keep) * f / factor + keep * f;
+        }
+        inv_freq[i] = g;
+    }
+    if (scale) *scale = kind == BI_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return BI_OK;
+}
+
+bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, void *q_out, int64_t q_out_token_stride,
+                          int64_t q_out_head_stride, int64_t Hq, const bi_paged_cache *cache,
+                          const int32_t *block_table, int64_t table_stride, int64_t max_pages,
+                          const int32_t *seq_lens, const int32_t *cu_new, const int32_t *positions,
+                          const double *inv_freq, int64_t R, bi_rope_layout layout, float scale, int64_t T,
+                          int64_t B, void *stream)
+{
+    bi_status st = check_cache(cache);
+    if (st != BI_OK) return st;
+    const int64_t D = cache->head_dim, Hkv = cache->heads;
+    if (T < 0 || B < 0 || max_pages < 0 || R < 0 || R > D || R % 2 != 0) return BI_ERR_INVALID_ARG;
+    if (layout != BI_ROPE_HALF && layout != BI_ROPE_INTERLEAVED) return BI_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || (q && Hq <= 0)) return BI_ERR_INVALID_ARG;
+    if (T > kI32Max || B >= kI32Max || max_pages > kI32Max || Hq > 65535) return BI_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return BI_OK;
+    if (!cu_new && T != B) return BI_ERR_INVALID_ARG;
+    if (!k || !v || !seq_lens || (max_pages > 0 && !block_table) || (R > 0 && !inv_freq)) return BI_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return BI_ERR_INVALID_ARG;
+    if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0) return BI_ERR_INVALID_ARG;
+    const int64_t qt = T > 1 && q ? q_token_stride : 0, qh = Hq > 1 && q ? q_head_stride : 0;
+    const int64_t qot = T > 1 && q ? q_out_token_stride : 0, qoh = Hq > 1 && q ? q_out_head_stride : 0;
+    if (q) {
+        if (qt < 0 || qh < 0 || (T > 1 && qot < D) || (Hq > 1 && qoh < D)) return BI_ERR_INVALID_ARG;
+        if (q == q_out && (qt != qot || qh != qoh)) return BI_ERR_INVALID_ARG;
+    }
+    for (const void *t : {k, v, q, static_cast<const void *>(q_out)})
+        if (reinterpret_cast<uintptr_t>(t) & 1u) return BI_ERR_ALIGNMENT;
+    for (const void *t : {block_table, seq_lens, cu_new, positions})
+        if (reinterpret_cast<uintptr_t>(t) & 3u) return BI_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(inv_freq) & 7u) return BI_ERR_ALIGNMENT;
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != BI_OK) return st;
+    bi::AppendParams p{};
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_cache = static_cast<__nv_bfloat16 *>(cache->k);
+    p.v_cache = static_cast<__nv_bfloat16 *>(cache->v);
+    p.k_token = T > 1 ? k_token_stride : 0;
+    p.k_head = Hkv > 1 ? k_head_stride : 0;
+    p.v_token = T > 1 ? v_token_stride : 0;
+    p.v_head = Hkv > 1 ? v_head_stride : 0;
+    p.q_token = qt;
+    p.q_head = qh;
+    p.qo_token = qot;
+    p.qo_head = qoh;
+    p.c_page = cache->pages > 1 ? cache->page_stride : 0;
+    p.c_token = cache->page_size > 1 ? cache->token_stride : 0;
+    p.c_head = Hkv > 1 ? cache->head_stride : 0;
+    p.table = block_table;
+    p.table_row = table_stride;
+    p.lens = seq_lens;
+    p.cu = cu_new;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.T = T;
+    p.pages = cache->pages;
+    p.B = (int32_t)B;
+    p.Hq = (int32_t)Hq;
+    p.Hkv = (int32_t)Hkv;
+    p.D = (int32_t)D;
+    p.R = (int32_t)R;
+    p.page_size = (int32_t)cache->page_size;
+    p.max_pages = (int32_t)max_pages;
+    p.scale = scale;
+    p.status = dev->status;
+    const bool pieces = rope_pieces(8, D, R) && strided_pieces(8, k, p.k_token, p.k_head) &&
+                        strided_pieces(8, v, p.v_token, p.v_head) && strided_pieces(8, q, qt, qh) &&
+                        strided_pieces(8, q_out, qot, qoh);
+    const bool half = layout == BI_ROPE_HALF;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return pieces ? launch_append<8>(p, half, dev->sms, s) : launch_append<1>(p, half, dev->sms, s);
+}
+
+size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len)
+{
+    if (B <= 0 || Hq <= 0 || D <= 0 || max_len <= bi::kPgSplit) return 0;
+    const size_t parts = (size_t)(B < bi::kPgSeqs ? B : bi::kPgSeqs) * (size_t)Hq * (size_t)bi::pg_splits(max_len);
+    return parts * ((size_t)D * sizeof(float) + sizeof(float2));
+}
+
+bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_paged_cache *cache,
+                                    const int32_t *block_table, int64_t table_stride, int64_t max_pages,
+                                    const int32_t *seq_lens, void *out, int64_t B, int64_t Hq, int64_t max_len,
+                                    float scale, void *scratch, size_t scratch_bytes, void *stream)
+{
+    bi_status st = check_cache(cache);
+    if (st != BI_OK) return st;
+    const int64_t D = cache->head_dim, Hkv = cache->heads;
+    if (B < 0 || Hq <= 0 || max_len <= 0 || max_pages <= 0 || Hq % Hkv != 0) return BI_ERR_INVALID_ARG;
+    const int64_t G = Hq / Hkv;
+    if ((D != 64 && D != 128) || G > 16) return BI_ERR_UNSUPPORTED;
+    if (B > 65535 || Hq > 65535 || max_len > kI32Max - bi::kPgSplit || max_pages > kI32Max) return BI_ERR_UNSUPPORTED;
+    if (max_len > max_pages * cache->page_size) return BI_ERR_INVALID_ARG;
+    const int64_t S = bi::pg_splits(max_len), Bl = B < bi::kPgSeqs ? B : bi::kPgSeqs;
+    if (Bl * S > kI32Max || Bl * S * Hkv > kI32Max) return BI_ERR_UNSUPPORTED;  // item numbers are 32-bit
+    if (B == 0) return BI_OK;
+    if (!q || !block_table || !seq_lens || !out || (S > 1 && !scratch)) return BI_ERR_INVALID_ARG;
+    if ((B > 1 && (q_stride < Hq * D || table_stride < max_pages))) return BI_ERR_INVALID_ARG;
+    if (scratch_bytes < bi_paged_decode_attention_scratch_bytes(B, Hq, D, max_len)) return BI_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (S > 1 && !aligned16(scratch)) || (B > 1 && q_stride % 8 != 0) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(block_table) & 3u))
+        return BI_ERR_ALIGNMENT;
+    DeviceState *dev = nullptr;
+    st = device_state(&dev);
+    if (st != BI_OK) return st;
+
+    bi::PgParams p{};
+    // A box is the largest run of a tile's tokens that never leaves a page.
+    int64_t box = cache->page_size, rest = bi::kPgTile;
+    while (rest != 0) {
+        const int64_t t = box % rest;
+        box = rest;
+        rest = t;
+    }
+    p.box = (int32_t)box;
+    p.heads_inner = cache->heads > 1 && (cache->page_size == 1 || cache->head_stride <= cache->token_stride) ? 1 : 0;
+    CUtensorMap tm_k, tm_v;
+    st = encode_page_map(&tm_k, cache->k, *cache, p.heads_inner != 0, (uint32_t)box);
+    if (st != BI_OK) return st;
+    st = encode_page_map(&tm_v, cache->v, *cache, p.heads_inner != 0, (uint32_t)box);
+    if (st != BI_OK) return st;
+    p.q_row = B > 1 ? q_stride : 0;
+    p.table_row = B > 1 ? table_stride : 0;
+    p.part_o = static_cast<float *>(scratch);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)(S > 1 ? Bl * Hq * S * D : 0));
+    p.Hq = (int32_t)Hq;
+    p.Hkv = (int32_t)Hkv;
+    p.G = (int32_t)G;
+    p.S = (int32_t)S;
+    p.page_size = (int32_t)cache->page_size;
+    p.pages = (int32_t)cache->pages;
+    p.max_len = (int32_t)max_len;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    p.status = dev->status;
+    p.wait_limit_ns = kWaitLimitNs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    for (int64_t b0 = 0; b0 < B; b0 += bi::kPgSeqs) {
+        p.B = (int32_t)(B - b0 < bi::kPgSeqs ? B - b0 : bi::kPgSeqs);
+        p.q = static_cast<const __nv_bfloat16 *>(q) + b0 * p.q_row;
+        p.out = static_cast<__nv_bfloat16 *>(out) + b0 * Hq * D;
+        p.lens = seq_lens + b0;
+        p.table = block_table + b0 * p.table_row;
+        // At most this many items; their true number is known on the device.
+        const int64_t items = (int64_t)p.B * Hkv * S;
+        const dim3 grid((unsigned)(items < dev->sms ? items : dev->sms));
+        if (D == 64)
+            st = G <= 8 ? launch_paged<64, 1>(grid, s, tm_k, tm_v, p) : launch_paged<64, 2>(grid, s, tm_k, tm_v, p);
+        else
+            st = G <= 8 ? launch_paged<128, 1>(grid, s, tm_k, tm_v, p) : launch_paged<128, 2>(grid, s, tm_k, tm_v, p);
+        if (st != BI_OK) return st;
+    }
+    return BI_OK;
+}
+
+bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const int32_t *tokens, float scale,
+                            int64_t top_k, float *logprobs, float *entropy, float *logsumexp, float *top_logprobs,
+                            int32_t *top_tokens, int64_t M, int64_t V, void *stream)
+{
+    if (M < 0 || V < 0 || top_k < 0) return BI_ERR_INVALID_ARG;
+    if (x_dtype != BI_BF16 && x_dtype != BI_F32) return BI_ERR_INVALID_ARG;
+    const double scale_log2 = (double)scale * 1.4426950408889634074;
+    if (!(scale > 0.0f) || !std::isfinite((float)scale_log2)) return BI_ERR_INVALID_ARG;
+    if (V > bi::kTlMaxV || top_k > bi::kTlMaxTop || M > kI32Max / bi::kTlMaxCluster) return BI_ERR_UNSUPPORTED;
+    if (M == 0) return BI_OK;
+    if (V == 0 || !x || ldx < V || top_k > V) return BI_ERR_INVALID_ARG;
+    if ((logprobs && !tokens) || (top_k > 0 && (!top_logprobs || !top_tokens))) return BI_ERR_INVALID_ARG;
+    const bool bf16 = x_dtype == BI_BF16;
+    if (reinterpret_cast<uintptr_t>(x) & (bf16 ? 1u : 3u)) return BI_ERR_ALIGNMENT;
+    for (const void *t : {static_cast<const void *>(tokens), static_cast<const void *>(logprobs),
+                          static_cast<const void *>(entropy), static_cast<const void *>(logsumexp),
+                          static_cast<const void *>(top_logprobs), static_cast<const void *>(top_tokens)})
+        if (reinterpret_cast<uintptr_t>(t) & 3u) return BI_ERR_ALIGNMENT;
+    DeviceState *dev = nullptr;
+    bi_status st = device_state(&dev);
+    if (st != BI_OK) return st;
+    bi::TlParams p{};
+    p.x = x;
+    p.ldx = ldx;
+    p.tokens = tokens;
+    p.scale = scale;
+    p.scale_log2 = (float)scale_log2;
+    p.V = (int32_t)V;
+    p.top = (int32_t)top_k;
+    p.pieces = (int32_t)((V + bi::tl_piece(bf16) - 1) / bi::tl_piece(bf16));
+    p.logprobs = logprobs;
+    p.entropy = entropy;
+    p.logsumexp = logsumexp;
+    p.top_logprobs = top_logprobs;
+    p.top_tokens = top_tokens;
+    p.status = dev->status;
+    // Blocks that share a row: as many as keep all rows resident at once (two blocks an SM), none idle.
+    p.cluster = bi::kTlMaxCluster;
+    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > 2 * (int64_t)dev->sms)) p.cluster /= 2;
+    const size_t smem = token_logprobs_smem((p.pieces + p.cluster - 1) / p.cluster, top_k);
+    const bool vec = aligned16(x) && (M == 1 || ldx % (bf16 ? 8 : 4) == 0);
+    void (*kernel)(bi::TlParams) = bf16 ? (vec ? bi::token_logprobs_kernel<true, true> : bi::token_logprobs_kernel<true, false>)
+                                        : (vec ? bi::token_logprobs_kernel<false, true> : bi::token_logprobs_kernel<false, false>);
+    return launch_pdl_clusters(kernel, (unsigned)(M * p.cluster), bi::kTlThreads, (unsigned)p.cluster, smem,
+                               static_cast<cudaStream_t>(stream), p);
+}
+
 bi_status bi_get_device_status(void *stream, int32_t *out)
 {
     if (!out) return BI_ERR_INVALID_ARG;
@@ -806,6 +1246,6 @@ void bi_tensor_map_cache_stats(int64_t *hits, int64_t *misses)
     if (misses) *misses = (int64_t)g_map_misses;
 }
 
-int32_t bi_version(void) { return 201; }
+int32_t bi_version(void) { return 300; }
 
 }  // extern "C"

@@ -1,0 +1,536 @@
+// paged_attention.cuh -- batch-invariant decode attention over a paged cache (one query token per
+// sequence).
+//
+// The cache is pages of P tokens; a sequence's block table names its pages in order.  Sequence b's
+// L_b tokens are cut into splits of kPgSplit tokens and each split into tiles of kPgTile tokens, cuts
+// fixed by the token's own place.  For each (split, kv head) the eight consumer warps of a CTA take a
+// tile each: scores, the tile's maximum, exp2 and the weighted value sum never leave the warp.  The
+// tiles of a split are then folded in tile order through shared memory; a sequence of one split is
+// written out at once, the splits of a longer one go to scratch and are folded by the second launch
+// in a tree fixed by the number of splits.  So a sequence's output depends on its own query, tokens
+// and length only.
+//
+// Bound by the cache's bytes.  One persistent CTA per SM; the (split, kv head) items of the batch are
+// numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
+// how ragged the batch is.  The producer warp fills a ring of tiles (K and V of 32 tokens: 16 KB at
+// head size 128, 10 tiles; 8 KB at 64, 20 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
+// entries, each within one page and completing on the tile's mbarrier.  The lanes look the item's
+// pages up one item ahead and each issues the boxes of its own pages.
+//
+// Tensor-core work (mma.sync m16n8k16, bf16 in, fp32 accumulate): S^T = K Q^T with tokens on the 16
+// rows and the group's heads on the 8 columns (two column tiles for groups of 9 to 16), then
+// O^T += V^T P^T with the head's entries on the rows.  The weights P enter as two bf16 terms (hi =
+// bf16(p), lo = bf16(p - hi), about 16 significant bits), so the only rounding to 8 bits is the
+// output's.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "attention.cuh"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace bi {
+
+constexpr int kPgTile = 32;                      // tokens per ring stage, one consumer warp's
+constexpr int kPgWarps = 8;                      // consumer warps
+constexpr int kPgSplit = kPgTile * kPgWarps;     // tokens per split
+constexpr int kPgThreads = 32 * (kPgWarps + 1);  // the last warp produces
+constexpr int kPgSeqs = 2048;                    // sequences per launch (their prefix sums are in shared memory)
+
+template <int D>
+struct PgShape {
+    static constexpr int kHalves = D / 64;                  // 64-entry TMA boxes per token row
+    static constexpr int kHalfBytes = kPgTile * 128;        // one half of a tile's K or V
+    static constexpr int kKBytes = kHalves * kHalfBytes;    // K (or V) of a tile
+    static constexpr int kStageBytes = 2 * kKBytes;
+    static constexpr int kStages = 160 * 1024 / kStageBytes;
+    static constexpr int kORow = D + 4;                     // floats between heads of a warp's sums: no bank conflicts
+    static constexpr int kOBytes = kPgWarps * 8 * kORow * 4;
+    static constexpr int kSmem = kStages * kStageBytes + kOBytes + 1024;  // + alignment slack
+};
+
+struct PgParams {
+    const __nv_bfloat16 *q;
+    int64_t q_row;  // entries between sequences
+    const int32_t *table;
+    int64_t table_row;
+    const int32_t *lens;
+    float *part_o;     // [B, Hq, S, D]
+    float2 *part_ml;   // [B, Hq, S] (maximum in units of log2, sum)
+    __nv_bfloat16 *out;  // [B, Hq, D]
+    int32_t B, Hq, Hkv, G, S, page_size, pages, max_len;
+    int32_t box;          // tokens per TMA box: gcd(page_size, kPgTile)
+    int32_t heads_inner;  // dimension order of the tensor maps: (entry, head, token, page) or (entry, token, head, page)
+    float scale_log2;     // score scale times log2(e)
+    int32_t *status;
+    uint64_t wait_limit_ns;
+};
+
+__host__ __device__ inline int64_t pg_splits(int64_t L) { return (L + kPgSplit - 1) / kPgSplit; }
+
+// Length as the kernels use it: outside 0 .. max_len it is clamped (and reported by the first launch).
+__device__ __forceinline__ int pg_len(int L, int max_len)
+{
+    return L < 0 ? 0 : (L > max_len ? max_len : L);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 8x8 b16 matrix in the mma register layout, transposed across the warp.
+__device__ __forceinline__ uint32_t movm_trans(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void pg_consumers_sync()
+{
+    asm volatile("barrier.sync 1, %0;" ::"n"(32 * kPgWarps) : "memory");
+}
+
+// Launch 1: grid = min(items, SMs).  Item i: kv head i % Hkv of the global split i / Hkv (kv head
+// fastest, so neighbouring CTAs read neighbouring pieces of the same tokens' rows).
+template <int D, int NT>  // NT column tiles of 8 query heads per kv head
+__global__ void __launch_bounds__(kPgThreads, 1)
+    paged_attention_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                                 const PgParams p)
+{
+    using C = PgShape<D>;
+    extern __shared__ uint8_t pg_raw[];
+    uint8_t *smem = pg_raw + ((1024u - (smem_addr(pg_raw) & 1023u)) & 1023u);
+    float *so_all = reinterpret_cast<float *>(smem + C::kStages * C::kStageBytes);  // [warp][8 heads][kORow]
+    __shared__ uint64_t full[C::kStages], empty[C::kStages];
+    __shared__ float red_m[kPgWarps][8 * NT], red_l[kPgWarps][8 * NT];
+    __shared__ int32_t first[kPgSeqs + 1];  // global number of each sequence's first split
+    __shared__ int32_t lens_s[kPgSeqs];
+    __shared__ int32_t warp_total[kPgWarps + 1];
+    __shared__ int abort_flag_s;
+    volatile int *abort_flag = &abort_flag_s;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        abort_flag_s = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();  // the previous kernel's output (q, cache, lengths, table) is complete
+    griddep_launch_dependents();
+
+    // Prefix sums of the split counts (an empty sequence counts as one split, which writes its zeros).
+    {
+        const int per = (p.B + kPgThreads - 1) / kPgThreads, b0 = tid * per;
+        int sum = 0;
+        for (int j = 0; j < per && b0 + j < p.B; ++j) {
+            const int given = p.lens[b0 + j], L = pg_len(given, p.max_len);
+            if (blockIdx.x == 0 && L != given) *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+            lens_s[b0 + j] = L;
+            const int n = (int)pg_splits(L);
+            sum += n > 0 ? n : 1;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) warp_total[warp] = inc;
+        __syncthreads();
+        int at = inc - sum;
+        for (int w = 0; w < warp; ++w) at += warp_total[w];
+        for (int j = 0; j < per && b0 + j < p.B; ++j) {
+            first[b0 + j] = at;
+            const int n = (int)pg_splits(lens_s[b0 + j]);
+            at += n > 0 ? n : 1;
+        }
+        if (b0 < p.B && b0 + per >= p.B) first[p.B] = at;
+    }
+    __syncthreads();
+
+    const uint32_t n_kv = (uint32_t)p.Hkv;
+    const uint32_t items = (uint32_t)first[p.B] * n_kv;
+    const uint64_t lim = p.wait_limit_ns;
+    struct Item {
+        int b, g, split, t0, n;  // n tokens from t0 on
+    };
+    auto item = [&](uint32_t it) -> Item {
+        const int sg = (int)(it / n_kv), g = (int)(it - (uint32_t)sg * n_kv);
+        const int b = warp_count_le(first, p.B, sg) - 1;
+        const int split = sg - first[b], t0 = split * kPgSplit;
+        const int left = lens_s[b] - t0;
+        return {b, g, split, t0, left < kPgSplit ? left : kPgSplit};
+    };
+
+    if (warp == kPgWarps) {
+        // ------------------------------------------------------------------ producer
+        const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
+        const int nb = kPgTile / p.box;                   // boxes per tile
+        constexpr int kRegs = kPgSplit / 32;              // boxes of an item per lane, at one token a box
+        int32_t page[kRegs], row[kRegs];
+        // Lane l holds boxes l, l + 32, ... of the item: their pages and the first row within.
+        auto look_up = [&](const Item &w, int32_t (&pg)[kRegs], int32_t (&rw)[kRegs]) {
+            const int boxes = (w.n + p.box - 1) / p.box;
+#pragma unroll
+            for (int r = 0; r < kRegs; ++r) {
+                const int k = lane + 32 * r;
+                pg[r] = 0;
+                rw[r] = 0;
+                if (32 * r < boxes && k < boxes) {
+                    const uint32_t t = (uint32_t)(w.t0 + k * p.box), c = t / (uint32_t)p.page_size;
+                    pg[r] = p.table[w.b * p.table_row + c];
+                    rw[r] = (int32_t)(t - c * (uint32_t)p.page_size);
+                }
+            }
+        };
+        uint32_t stage = 0, phase = 0;
+        int issued = 0;
+        bool ok = true;
+        Item w{};
+        if (blockIdx.x < items) {
+            w = item(blockIdx.x);
+            look_up(w, page, row);
+        }
+        for (uint32_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            Item wn{};
+            int32_t page_n[kRegs], row_n[kRegs];
+            const bool more = it + gridDim.x < items;
+            if (more) {
+                wn = item(it + gridDim.x);
+                look_up(wn, page_n, row_n);
+            }
+            const int boxes = (w.n + p.box - 1) / p.box, tiles = (w.n + kPgTile - 1) / kPgTile;
+            for (int j = 0; j < tiles; ++j) {
+                ok = __all_sync(0xffffffffu, wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status, lim));
+                if (!ok) break;
+                const int k0 = j * nb, cnt = boxes - k0 < nb ? boxes - k0 : nb;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(cnt * p.box * D * 2 * 2));
+                __syncwarp();
+                const int r = k0 >> 5, x = lane - (k0 & 31);
+                int32_t pg = page[0], rw = row[0];
+#pragma unroll
+                for (int q = 1; q < kRegs; ++q)
+                    if (r == q) {
+                        pg = page[q];
+                        rw = row[q];
+                    }
+                if (x >= 0 && x < cnt) {
+                    if (pg < 0 || pg >= p.pages) {  // no such page: recorded, and read as zeros (out of the map's range)
+                        *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                        pg = p.pages;
+                    }
+                    uint8_t *dst = smem + stage * C::kStageBytes + x * p.box * 128;
+                    const int c1 = p.heads_inner ? w.g : rw, c2 = p.heads_inner ? rw : w.g;
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_4d(dst + h * C::kHalfBytes, &tm_k, &full[stage], 64 * h, c1, c2, pg, policy);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_4d(dst + C::kKBytes + h * C::kHalfBytes, &tm_v, &full[stage], 64 * h, c1, c2, pg, policy);
+                }
+                ++issued;
+                advance(stage, phase, C::kStages);
+            }
+            if (more) {
+                w = wn;
+#pragma unroll
+                for (int r = 0; r < kRegs; ++r) {
+                    page[r] = page_n[r];
+                    row[r] = row_n[r];
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // A wait ran out: let every copy already issued land before shared memory goes away.
+            for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(smem_addr(&full[j % C::kStages]), (uint32_t)(j / C::kStages) & 1u) &&
+                       global_timer_ns() - t0 < lim) {
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------ consumers
+        // Warp w takes tile w of every item.  Tiles are numbered across the CTA's items; tile number n
+        // sits in stage n % kStages.  Every warp has passed the previous item's barriers, so all its
+        // tiles have landed, and a stage's previous tile belongs to an earlier item (an item has at
+        // most 8 tiles): the parity waited for is the stage's next one.
+        const int gid = lane >> 2, tig = lane & 3;
+        uint32_t base = 0;
+        bool alive = true;
+        float *so = so_all + warp * 8 * C::kORow;
+        for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
+            const Item w = item(it);
+            const int tiles = (w.n + kPgTile - 1) / kPgTile;
+            const int head0 = w.g * p.G;
+            if (w.n <= 0) {  // an empty sequence: its row is zeros
+                __nv_bfloat16 *o = p.out + ((int64_t)w.b * p.Hq + head0) * D;
+                for (int i = tid; i < p.G * D / 8; i += 32 * kPgWarps) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const uint32_t num = base + (uint32_t)warp;
+            base += (uint32_t)tiles;
+            const bool mine = warp < tiles;
+            float m[NT][2], l[NT][2];  // of heads 8 nt + 2 tig and + 1
+            float o[NT][D / 16][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                m[nt][0] = m[nt][1] = kNegInf;
+                l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
+            }
+            if (mine && alive) {
+                // Q^T fragments: column n = head, rows k = entries 16 kk + 2 tig (+1) and + 8.
+                uint32_t qf[NT][D / 16][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const bool live = 8 * nt + gid < p.G;
+                    const __nv_bfloat16 *qr = p.q + w.b * p.q_row + (int64_t)(head0 + 8 * nt + gid) * D + 2 * tig;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        qf[nt][kk][0] = live ? *reinterpret_cast<const uint32_t *>(qr + 16 * kk) : 0u;
+                        qf[nt][kk][1] = live ? *reinterpret_cast<const uint32_t *>(qr + 16 * kk + 8) : 0u;
+                    }
+                }
+                const uint32_t stage = num % C::kStages, use = num / C::kStages;
+                alive = __all_sync(0xffffffffu, wait_bounded(&full[stage], use & 1u, abort_flag, p.status, lim));
+                if (alive) {
+                    const uint8_t *ks = smem + stage * C::kStageBytes, *vs = ks + C::kKBytes;
+                    const int n_tok = w.n - kPgTile * warp < kPgTile ? w.n - kPgTile * warp : kPgTile;
+                    // 16-byte chunk c of token row r: 128-byte swizzle within each 64-entry half.
+                    auto chunk = [&](const uint8_t *t, int r, int c) {
+                        return t + (c >> 3) * C::kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    };
+                    // ---- scores of tokens 16 mt + gid (+ 8) and heads 8 nt + 2 tig (+ 1)
+                    float s[NT][2][4];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) s[nt][mt][0] = s[nt][mt][1] = s[nt][mt][2] = s[nt][mt][3] = 0.0f;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            uint32_t a[4];
+                            ldsm_x4(a, chunk(ks, 16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[nt][mt], a, qf[nt][kk][0], qf[nt][kk][1]);
+                        }
+                    }
+                    // ---- the tile's maximum and weights; tokens past the sequence weigh nothing
+                    uint32_t hi[NT][2][2], lo[NT][2][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float &x = s[nt][mt][e];
+                                x = 16 * mt + gid + 8 * (e >> 1) < n_tok ? __fmul_rn(x, p.scale_log2) : kNegInf;
+                                m[nt][e & 1] = fmaxf(m[nt][e & 1], x);
+                            }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float v = m[nt][c];
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                            m[nt][c] = v;
+                            const float ref = v == kNegInf ? 0.0f : v;
+                            float sum = 0.0f;
+#pragma unroll
+                            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float &x = s[nt][mt][2 * r + c];
+                                    x = ex2(x - ref);
+                                    sum = __fadd_rn(sum, x);
+                                }
+                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 4));
+                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 8));
+                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 16));
+                            l[nt][c] = sum;
+                        }
+                        // Weights as two bf16 terms, turned so that tokens run along a thread's registers.
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float x = s[nt][mt][2 * r], y = s[nt][mt][2 * r + 1];
+                                const float xh = __bfloat162float(__float2bfloat16_rn(x));
+                                const float yh = __bfloat162float(__float2bfloat16_rn(y));
+                                hi[nt][mt][r] = movm_trans(pack_bf16(xh, yh));
+                                lo[nt][mt][r] = movm_trans(pack_bf16(x - xh, y - yh));
+                            }
+                    }
+                    // ---- O^T += V^T P^T over two 16-token steps in ascending order, hi before lo
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        // Value rows past the sequence hold anything: their bits are cleared.
+                        const int ta = 16 * mt + 2 * tig;
+                        uint32_t keep[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            keep[r] = (ta + 8 * r < n_tok ? 0xffffu : 0u) | (ta + 8 * r + 1 < n_tok ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int dt = 0; dt < D / 8; dt += 2) {
+                            uint32_t v[4];
+                            ldsm_x4_trans(v, chunk(vs, 16 * mt + (lane & 15), dt + (lane >> 4)));
+                            const uint32_t a[4] = {v[0] & keep[0], v[2] & keep[0], v[1] & keep[1], v[3] & keep[1]};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_16816_bf16(o[nt][dt / 2], a, hi[nt][mt][0], hi[nt][mt][1]);
+                                mma_16816_bf16(o[nt][dt / 2], a, lo[nt][mt][0], lo[nt][mt][1]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[stage]);
+                }
+            }
+            // ---- fold the tiles in order: heads 8 nt .. 8 nt + 7 at a time through shared memory
+            if (gid == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        red_m[warp][8 * nt + 2 * tig + c] = m[nt][c];
+                        red_l[warp][8 * nt + 2 * tig + c] = l[nt][c];
+                    }
+            }
+            const bool last = first[w.b + 1] - first[w.b] == 1;  // the sequence's only split
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int heads = p.G - 8 * nt < 8 ? p.G - 8 * nt : 8;
+                if (mine) {
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int head = 2 * tig + (e & 1), d = 16 * mt + gid + 8 * (e >> 1);
+                            if (head < heads) so[head * C::kORow + d] = o[nt][mt][e];
+                        }
+                }
+                pg_consumers_sync();
+                for (int i = tid; i < heads * (D / 4); i += 32 * kPgWarps) {
+                    const int hl = i / (D / 4), d = 4 * (i % (D / 4)), h = 8 * nt + hl;
+                    float mx = red_m[0][h];
+                    for (int t = 1; t < tiles; ++t) mx = fmaxf(mx, red_m[t][h]);
+                    const float ref = mx == kNegInf ? 0.0f : mx;
+                    float sum = 0.0f;
+                    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int t = 0; t < tiles; ++t) {
+                        const float f = ex2(red_m[t][h] - ref);
+                        const float4 v = *reinterpret_cast<const float4 *>(so_all + (t * 8 + hl) * C::kORow + d);
+                        sum = __fmaf_rn(red_l[t][h], f, sum);
+                        r.x = __fmaf_rn(v.x, f, r.x);
+                        r.y = __fmaf_rn(v.y, f, r.y);
+                        r.z = __fmaf_rn(v.z, f, r.z);
+                        r.w = __fmaf_rn(v.w, f, r.w);
+                    }
+                    const int64_t bh = (int64_t)w.b * p.Hq + head0 + h;
+                    if (last) {
+                        uint2 u;
+                        u.x = pack_bf16(r.x / sum, r.y / sum);
+                        u.y = pack_bf16(r.z / sum, r.w / sum);
+                        *reinterpret_cast<uint2 *>(p.out + bh * D + d) = u;
+                    } else {
+                        *reinterpret_cast<float4 *>(p.part_o + (bh * p.S + w.split) * D + d) = r;
+                        if (d == 0) p.part_ml[bh * p.S + w.split] = make_float2(mx, sum);
+                    }
+                }
+                pg_consumers_sync();
+            }
+        }
+    }
+}
+
+// Launch 2: grid (Hq, B), 256 threads.  The block's 1024 / D groups of D/4 lanes take the splits s, s +
+// groups, ... in ascending order, four columns a lane; the groups are then folded in order.
+constexpr int kPgCombineThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kPgCombineThreads)
+    paged_attention_combine_kernel(const float2 *__restrict__ part_ml, const float *__restrict__ part_o,
+                                   const int32_t *__restrict__ lens, __nv_bfloat16 *__restrict__ out, int Hq, int S,
+                                   int max_len)
+{
+    constexpr int kLanes = D / 4, kGroups = kPgCombineThreads / kLanes, kAhead = 4;
+    __shared__ float red[kPgCombineThreads / 32], sl[kGroups];
+    __shared__ float4 so[kGroups][kLanes];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, grp = tid / kLanes, c = tid % kLanes;
+    const int n = (int)pg_splits(pg_len(lens[b], max_len));
+    if (n <= 1) return;  // written by launch 1
+    const int64_t bh = (int64_t)b * Hq + h;
+    const float2 *ml = part_ml + bh * S;
+    const float4 *po = reinterpret_cast<const float4 *>(part_o + bh * S * D) + c;
+    // The first values are on their way while the maximum (exact in any order) is found.
+    float4 v[kAhead];
+    float2 w[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int s = grp + k * kGroups;
+        v[k] = s < n ? po[(int64_t)s * kLanes] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
+    }
+    float m = kNegInf;
+    for (int s = tid; s < n; s += kPgCombineThreads) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int k = 1; k < kPgCombineThreads / 32; ++k) m = fmaxf(m, red[k]);
+    const float ref = m == kNegInf ? 0.0f : m;
+    float l = 0.0f;
+    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = grp; s0 < n; s0 += kAhead * kGroups) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float f = ex2(w[k].x - ref);  // 0 past the last split
+            l = __fmaf_rn(w[k].y, f, l);
+            r.x = __fmaf_rn(v[k].x, f, r.x);
+            r.y = __fmaf_rn(v[k].y, f, r.y);
+            r.z = __fmaf_rn(v[k].z, f, r.z);
+            r.w = __fmaf_rn(v[k].w, f, r.w);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int s = s0 + (kAhead + k) * kGroups;
+            v[k] = s < n ? po[(int64_t)s * kLanes] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
+        }
+    }
+    so[grp][c] = r;
+    if (c == 0) sl[grp] = l;
+    __syncthreads();
+    if (tid < kLanes) {
+        r = so[0][c];
+        l = sl[0];
+        for (int g = 1; g < kGroups; ++g) {
+            l = __fadd_rn(l, sl[g]);
+            r.x = __fadd_rn(r.x, so[g][c].x);
+            r.y = __fadd_rn(r.y, so[g][c].y);
+            r.z = __fadd_rn(r.z, so[g][c].z);
+            r.w = __fadd_rn(r.w, so[g][c].w);
+        }
+        uint2 u;
+        u.x = pack_bf16(r.x / l, r.y / l);
+        u.y = pack_bf16(r.z / l, r.w / l);
+        *reinterpret_cast<uint2 *>(out + bh * D + 4 * c) = u;
+    }
+}
+
+}  // namespace bi

@@ -1,0 +1,325 @@
+// token_logprobs.cuh -- per row of logits: the log-probability of a given token, the entropy, the log of
+// the sum of exponentials and the k best alternatives, in one pass that writes no probabilities.
+//
+// With z = scale * x, m = max x, d = z - scale m and e = exp(d):
+//   S = sum e,  T = sum e d,  logsumexp = scale m + log S,  logprob(t) = d_t - log S,
+//   entropy = log S - T / S   (a term with e = 0 adds nothing, so -inf logits are allowed).
+//
+// Order (fixed by V and the type alone): the row is cut into pieces; in a piece each thread of the
+// block owns 64 consecutive bytes (32 bf16 or 16 fp32 elements, a group).  A warp takes the maximum of
+// its elements, then every thread's sums of e and e d over its group (two interleaved chains), then a
+// fixed butterfly: one (m, S, T) per (piece, warp).  These are folded at the end by one warp:
+// lane j folds triples j, j + 32, ... in order, then a fixed butterfly.  A row is taken by one block or
+// by a cluster of 2, 4 or 8 that share its pieces; the triples, and so the bits, are the same.
+//
+// The k best: only the groups' maxima are kept during the pass.
+// The k best elements lie in the k best groups (larger maximum first, lower group first among equals,
+// as groups are consecutive), so the end of the row reads a few groups again instead of sorting.  What
+// is compared are 64-bit keys (ordered value, inverted index): ties go to the lowest token, and the
+// result does not depend on the order in which keys are met.  NaN counts as less than every number.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+#include "rowops.cuh"
+
+namespace bi {
+
+constexpr int kTlThreads = 512;
+constexpr int kTlWarps = kTlThreads / 32;
+constexpr int kTlWords = 16;                        // 32-bit words per thread and piece
+constexpr int kTlMaxV = 262144;
+constexpr int kTlMaxTop = 32;
+constexpr int kTlMaxCluster = 8;
+
+__host__ __device__ constexpr int tl_group(bool bf16) { return bf16 ? 2 * kTlWords : kTlWords; }
+__host__ __device__ constexpr int tl_piece(bool bf16) { return kTlThreads * tl_group(bf16); }  // 16384 or 8192
+constexpr int kTlMaxPieces = kTlMaxV / tl_piece(false);
+
+struct TlParams {
+    const void *x;
+    int64_t ldx;
+    const int32_t *tokens;  // may be null
+    float scale;            // multiplies the logits
+    float scale_log2;       // scale * log2(e)
+    int32_t V, top, pieces, cluster;
+    float *logprobs, *entropy, *logsumexp;  // each may be null
+    float *top_logprobs;    // [M, top]
+    int32_t *top_tokens;
+    int32_t *status;
+};
+
+struct TlTriple {
+    float m, s, t;  // maximum of x, sum of e, sum of e * d in units of log2
+};
+
+// Symmetric in its arguments, so both lanes of a butterfly pair hold equal bits.
+__device__ __forceinline__ TlTriple tl_merge(TlTriple a, TlTriple b, float c)
+{
+    const float m = fmaxf(a.m, b.m), ref = m == kNegInf ? 0.0f : m;
+    // A side whose maximum is -inf has no terms: its offset is set to 0, its factor meets sums of 0.
+    const float da = a.m == kNegInf ? 0.0f : __fmul_rn(a.m - ref, c), db = b.m == kNegInf ? 0.0f : __fmul_rn(b.m - ref, c);
+    const float fa = exp2f(da), fb = exp2f(db);
+    // d grows by da: T' = f (T + s da).  With da = -inf (a range beyond fp32) f is 0 and the side is dropped.
+    const float ta = fa == 0.0f ? 0.0f : __fmul_rn(fa, __fadd_rn(a.t, __fmul_rn(a.s, da)));
+    const float tb = fb == 0.0f ? 0.0f : __fmul_rn(fb, __fadd_rn(b.t, __fmul_rn(b.s, db)));
+    return {m, __fadd_rn(__fmul_rn(fa, a.s), __fmul_rn(fb, b.s)), __fadd_rn(ta, tb)};
+}
+
+// Ascending with the value; -0 as +0, NaN below everything.
+__device__ __forceinline__ uint32_t tl_order(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    if (v != v) return 0u;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float tl_value(uint32_t o)
+{
+    return __uint_as_float(o == 0u ? 0x7fffffffu : o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t tl_key(float v, uint32_t index)
+{
+    return (uint64_t)tl_order(v) << 32 | (uint32_t)~index;  // never 0: indices are below 2^31
+}
+
+// The warp's list of the largest keys, one per lane, descending (0: none yet); `k` of them count.
+struct TlList {
+    uint64_t mine = 0, kth = 0;
+    // Offers one key per lane (0: none).
+    __device__ __forceinline__ void offer(uint64_t key, int k)
+    {
+        const int lane = threadIdx.x & 31;
+        unsigned better = __ballot_sync(0xffffffffu, key > kth);
+        while (better) {
+            const int src = __ffs(better) - 1;
+            const uint64_t b = __shfl_sync(0xffffffffu, key, src);
+            const int rank = __popc(__ballot_sync(0xffffffffu, mine > b));
+            const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+            if (lane == rank) mine = b;
+            else if (lane > rank) mine = up;
+            kth = __shfl_sync(0xffffffffu, mine, k - 1);
+            if (lane == src) key = 0;
+            better = __ballot_sync(0xffffffffu, key > kth);
+        }
+    }
+};
+
+// d + {c, c} etc. on pairs of fp32 (one instruction on sm_100a).
+__device__ __forceinline__ uint64_t f2_pack(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A thread's group as it sits in memory.
+template <bool BF16>
+struct TlGroup {
+    static constexpr int kSize = tl_group(BF16);
+    uint32_t w[kTlWords];
+
+    // Elements e0 .. e0 + kSize - 1 of a row of V; elements past V are -inf.  VEC: rows are 16-byte aligned.
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void *row, int e0, int V)
+    {
+        if (VEC && e0 + kSize <= V) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + (int64_t)e0 * (BF16 ? 2 : 4));
+#pragma unroll
+            for (int i = 0; i < kTlWords / 4; ++i) {
+                const uint4 v = __ldcs(src + i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kTlWords; ++i) {
+            if (BF16) {
+                const uint16_t *src = static_cast<const uint16_t *>(row) + e0 + 2 * i;
+                const uint32_t a = e0 + 2 * i < V ? src[0] : 0xff80u, b = e0 + 2 * i + 1 < V ? src[1] : 0xff80u;
+                w[i] = a | b << 16;
+            } else {
+                w[i] = e0 + i < V ? static_cast<const uint32_t *>(row)[e0 + i] : 0xff800000u;
+            }
+        }
+    }
+    __device__ __forceinline__ float2 pair(int i) const  // elements 2 i and 2 i + 1
+    {
+        if (BF16) return make_float2(bf16lo(w[i]), bf16hi(w[i]));
+        return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    __device__ __forceinline__ float max() const
+    {
+        float m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < TlGroup<BF16>::kSize / 2; ++i) {
+            const float2 v = pair(i);
+            m = fmaxf(m, fmaxf(v.x, v.y));
+        }
+        return m;
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float tl_element(const void *row, int e)
+{
+    if (BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]);
+    return static_cast<const float *>(row)[e];
+}
+
+// Grid M * cluster blocks of kTlThreads; block r of a row's cluster takes pieces r, r + cluster, ...
+// Dynamic shared memory: the block's group maxima, kTlThreads floats per piece (top > 0 only).
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlParams p)
+{
+    namespace cg = cooperative_groups;
+    constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
+    extern __shared__ float tl_max[];  // [pieces of this block][kTlThreads]
+    __shared__ TlTriple triple[kTlMaxPieces * kTlWarps];
+    __shared__ uint64_t best[kTlMaxCluster][kTlMaxTop];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)(blockIdx.x % (unsigned)p.cluster);
+    const int64_t r = blockIdx.x / (unsigned)p.cluster;
+    const void *row = static_cast<const uint8_t *>(p.x) + r * p.ldx * (BF16 ? 2 : 4);
+    TlTriple *triples = triple;
+    uint64_t(*bests)[kTlMaxTop] = best;
+    if (p.cluster > 1) {
+        triples = cg::this_cluster().map_shared_rank(triple, 0);
+        bests = reinterpret_cast<uint64_t(*)[kTlMaxTop]>(cg::this_cluster().map_shared_rank(&best[0][0], 0));
+        cluster_sync_all();  // every block of the cluster runs before its shared memory is written
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    TlGroup<BF16> g, next;
+    int local = 0;
+    if (rank < p.pieces) g.template load<VEC>(row, rank * kPiece + kGroup * tid, p.V);
+    for (int piece = rank; piece < p.pieces; piece += p.cluster, ++local) {
+        const int ahead = piece + p.cluster;
+        if (ahead < p.pieces) next.template load<VEC>(row, ahead * kPiece + kGroup * tid, p.V);
+        const float gm = g.max();
+        if (p.top > 0) tl_max[local * kTlThreads + tid] = gm;
+        float m = gm;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m == kNegInf ? 0.0f : m;
+        const uint64_t neg = f2_pack(-ref, -ref);
+        uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+        for (int i = 0; i < TlGroup<BF16>::kSize / 2; ++i) {
+            const float2 v = g.pair(i);
+            const uint64_t d2 = f2_mul(f2_add(f2_pack(v.x, v.y), neg), c2);
+            const float2 d = f2_unpack(d2);
+            float ex, ey;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(d.x));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(d.y));
+            const uint64_t e2 = f2_pack(ex, ey);
+            s2 = f2_add(s2, e2);
+            // -inf would make 0 * -inf: below -1000 the factor is 0 already.
+            t2 = f2_fma(e2, f2_pack(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f)), t2);
+        }
+        const float2 sv = f2_unpack(s2), tv = f2_unpack(t2);
+        const float s = warp_sum(__fadd_rn(sv.x, sv.y)), t = warp_sum(__fadd_rn(tv.x, tv.y));
+        if (lane == 0) triples[piece * kTlWarps + warp] = TlTriple{m, s, t};
+        g = next;
+    }
+    __syncthreads();
+
+    // The block's best keys: warp 0 walks the group maxima in index order and reads again only the
+    // groups that beat the k-th key so far.
+    if (p.top > 0 && warp == 0) {
+        TlList list;
+        for (int i0 = 0; i0 < local * kTlThreads; i0 += 32) {
+            const int i = i0 + lane;
+            const int e0 = ((i / kTlThreads) * p.cluster + rank) * kPiece + kGroup * (i % kTlThreads);
+            const uint64_t gk = e0 < p.V ? tl_key(tl_max[i], (uint32_t)e0) : 0;
+            unsigned better = __ballot_sync(0xffffffffu, gk > list.kth);
+            while (better) {
+                const int src = __ffs(better) - 1;
+                const int e = __shfl_sync(0xffffffffu, e0, src) + lane;
+                list.offer(lane < kGroup && e < p.V ? tl_key(tl_element<BF16>(row, e), (uint32_t)e) : 0, p.top);
+                better &= better - 1;
+                better &= __ballot_sync(0xffffffffu, gk > list.kth);
+            }
+        }
+        bests[rank][lane] = list.mine;
+    }
+    if (p.cluster > 1) {
+        cluster_sync_all();
+        if (rank != 0) return;
+    } else {
+        __syncwarp();
+    }
+    if (warp != 0) return;
+
+    TlTriple a{kNegInf, 0.0f, 0.0f};
+    for (int i = lane; i < p.pieces * kTlWarps; i += 32) a = tl_merge(a, triple[i], p.scale_log2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const TlTriple b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                         __shfl_xor_sync(0xffffffffu, a.t, o)};
+        a = tl_merge(a, b, p.scale_log2);
+    }
+    // A row without a finite maximum has no distribution: all its values are NaN.
+    const float log_s = logf(a.s);
+    auto logprob = [&](float x) { return __fsub_rn(__fmul_rn(x - a.m, p.scale), log_s); };
+    if (lane == 0) {
+        if (p.logprobs != nullptr) {
+            const int32_t tok = p.tokens[r];
+            float v = 0.0f;  // a negative token: the row is not scored
+            if (tok >= p.V) {
+                *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                v = __int_as_float(0x7fffffff);
+            } else if (tok >= 0) {
+                v = logprob(tl_element<BF16>(row, tok));
+            }
+            p.logprobs[r] = v;
+        }
+        if (p.entropy != nullptr) p.entropy[r] = __fsub_rn(log_s, __fmul_rn(0.693147180559945309f, a.t / a.s));
+        if (p.logsumexp != nullptr) p.logsumexp[r] = __fmaf_rn(a.m, p.scale, log_s);
+    }
+    if (p.top > 0) {
+        TlList list;
+        if (p.cluster > 1) {
+            for (int q = 0; q < p.cluster; ++q) list.offer(lane < p.top ? best[q][lane] : 0, p.top);
+        } else {
+            list.mine = best[0][lane];
+        }
+        if (lane < p.top) {
+            p.top_logprobs[r * p.top + lane] = logprob(tl_value((uint32_t)(list.mine >> 32)));
+            p.top_tokens[r * p.top + lane] = (int32_t)~(uint32_t)list.mine;
+        }
+    }
+}
+
+}  // namespace bi
