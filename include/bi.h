@@ -395,8 +395,8 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
  * Passage: as bi_decode_attention.
  *
  * Batch invariance: a sequence is cut into splits of 256 tokens and tiles of 32, cuts fixed by the token's
- * own place; a tile's scores are fp32 dot products, its weights relative to its own maximum; tiles fold in
- * order within a split, and splits in a tree fixed by their number.  A sequence's output does not depend on
+ * own place; scores are fp32 dot products, four chains take the split's tiles w and w + 4 under a running
+ * maximum and are folded in order, and splits in a tree fixed by their number.  A sequence's output does not depend on
  * the others, on where its pages lie, on the page size or on max_len.
  *
  *   q        device, bf16, [B, Hq, D], heads consecutive, sequences q_stride elements apart (a multiple of 8).

@@ -3,16 +3,17 @@
 //
 // The cache is pages of P tokens; a sequence's block table names its pages in order.  Sequence b's
 // L_b tokens are cut into splits of kPgSplit tokens and each split into tiles of kPgTile tokens, cuts
-// fixed by the token's own place.  For each (split, kv head) the eight consumer warps of a CTA take a
-// tile each: scores, the tile's maximum, exp2 and the weighted value sum never leave the warp.  The
-// tiles of a split are then folded in tile order through shared memory; a sequence of one split is
+// fixed by the token's own place.  A (split, kv head) is taken by a group of four warps: warp w takes tiles w and
+// w + 4, with a running maximum; scores, weights and the weighted value sum never leave the warp.  The
+// four warps are then folded in order through shared memory; a sequence of one split is
 // written out at once, the splits of a longer one go to scratch and are folded by the second launch
 // in a tree fixed by the number of splits.  So a sequence's output depends on its own query, tokens
 // and length only.
 //
 // Bound by the cache's bytes.  One persistent CTA per SM; the (split, kv head) items of the batch are
 // numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
-// how ragged the batch is.  The producer warp fills a ring of tiles (K and V of 32 tokens: 16 KB at
+// how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
+// other's arithmetic and loads.  The producer warp fills a ring of tiles (K and V of 32 tokens: 16 KB at
 // head size 128, 10 tiles; 8 KB at 64, 20 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
 // entries, each within one page and completing on the tile's mbarrier.  The lanes look the item's
 // pages up one item ahead and each issues the boxes of its own pages.
@@ -36,7 +37,9 @@ namespace bi {
 
 constexpr int kPgTile = 32;                      // tokens per ring stage, one consumer warp's
 constexpr int kPgWarps = 8;                      // consumer warps
-constexpr int kPgSplit = kPgTile * kPgWarps;     // tokens per split
+constexpr int kPgGroups = 2;                     // consumer groups, alternate items
+constexpr int kPgGroupWarps = kPgWarps / kPgGroups;
+constexpr int kPgSplit = 256;                    // tokens per split: two tiles for each warp of a group
 constexpr int kPgThreads = 32 * (kPgWarps + 1);  // the last warp produces
 constexpr int kPgSeqs = 2048;                    // sequences per launch (their prefix sums are in shared memory)
 
@@ -92,11 +95,6 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
     return y;
 }
 
-__device__ __forceinline__ void pg_consumers_sync()
-{
-    asm volatile("barrier.sync 1, %0;" ::"n"(32 * kPgWarps) : "memory");
-}
-
 // Launch 1: grid = min(items, SMs).  Item i: kv head i % Hkv of the global split i / Hkv (kv head
 // fastest, so neighbouring CTAs read neighbouring pieces of the same tokens' rows).
 template <int D, int NT>  // NT column tiles of 8 query heads per kv head
@@ -114,13 +112,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __shared__ int32_t lens_s[kPgSeqs];
     __shared__ int32_t warp_total[kPgWarps + 1];
     __shared__ int abort_flag_s;
-    volatile int *abort_flag = &abort_flag_s;
+    __shared__ int slot_use_s[C::kStages];  // uses of each stage that a consumer warp has passed
+    volatile int *abort_flag = &abort_flag_s, *slot_use = slot_use_s;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            slot_use_s[s] = 0;
         }
         abort_flag_s = 0;
         fence_mbar_init();
@@ -261,27 +261,30 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ consumers
-        // Warp w takes tile w of every item.  Tiles are numbered across the CTA's items; tile number n
-        // sits in stage n % kStages.  Every warp has passed the previous item's barriers, so all its
-        // tiles have landed, and a stage's previous tile belongs to an earlier item (an item has at
-        // most 8 tiles): the parity waited for is the stage's next one.
+        // Group grp takes the CTA's items grp, grp + 2, ...; its warp cw tiles cw and cw + 4 of each.  Tiles are
+        // numbered across all of the CTA's items in the producer's order; tile number n is use n / kStages of stage
+        // n % kStages.  A stage's uses are passed in order: once its previous use has been passed (slot_use, by
+        // either group) its barrier is at most one phase from the one waited for, so a parity wait is exact.
+        const int grp = warp / kPgGroupWarps, cw = warp % kPgGroupWarps, ct = tid % (32 * kPgGroupWarps);
         const int gid = lane >> 2, tig = lane & 3;
-        uint32_t base = 0;
+        uint32_t base = 0, local = 0;
         bool alive = true;
-        float *so = so_all + warp * 8 * C::kORow;
+        float *so_grp = so_all + grp * kPgGroupWarps * 8 * C::kORow, *so = so_grp + cw * 8 * C::kORow;
+        float(*gm)[8 * NT] = red_m + grp * kPgGroupWarps, (*gl)[8 * NT] = red_l + grp * kPgGroupWarps;
         for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
             const Item w = item(it);
             const int tiles = (w.n + kPgTile - 1) / kPgTile;
             const int head0 = w.g * p.G;
+            const uint32_t num0 = base;
+            base += (uint32_t)tiles;
+            if ((int)(local++ % kPgGroups) != grp) continue;
             if (w.n <= 0) {  // an empty sequence: its row is zeros
                 __nv_bfloat16 *o = p.out + ((int64_t)w.b * p.Hq + head0) * D;
-                for (int i = tid; i < p.G * D / 8; i += 32 * kPgWarps) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
+                for (int i = ct; i < p.G * D / 8; i += 32 * kPgGroupWarps) reinterpret_cast<uint4 *>(o)[i] = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            const uint32_t num = base + (uint32_t)warp;
-            base += (uint32_t)tiles;
-            const bool mine = warp < tiles;
-            float m[NT][2], l[NT][2];  // of heads 8 nt + 2 tig and + 1
+            const int warps = tiles < kPgGroupWarps ? tiles : kPgGroupWarps;  // with a tile of this item
+            float m[NT][2], l[NT][2];  // of heads 8 nt + 2 tig and + 1; l of this thread's tokens only
             float o[NT][D / 16][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
             }
-            if (mine && alive) {
+            if (cw < warps) {
                 // Q^T fragments: column n = head, rows k = entries 16 kk + 2 tig (+1) and + 8.
                 uint32_t qf[NT][D / 16][2];
 #pragma unroll
@@ -303,11 +306,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         qf[nt][kk][1] = live ? *reinterpret_cast<const uint32_t *>(qr + 16 * kk + 8) : 0u;
                     }
                 }
-                const uint32_t stage = num % C::kStages, use = num / C::kStages;
-                alive = __all_sync(0xffffffffu, wait_bounded(&full[stage], use & 1u, abort_flag, p.status, lim));
-                if (alive) {
+#pragma unroll 1
+                for (int j = cw; j < tiles; j += kPgGroupWarps) {
+                    const uint32_t num = num0 + (uint32_t)j, stage = num % C::kStages, use = num / C::kStages;
+                    if (alive)
+                        alive = __all_sync(0xffffffffu,
+                                           wait_flag_at_least(&slot_use[stage], (int)use, abort_flag, p.status, lim) &&
+                                               wait_bounded(&full[stage], use & 1u, abort_flag, p.status, lim));
+                    if (!alive) break;
+                    if (lane == 0) slot_use[stage] = (int)use + 1;
                     const uint8_t *ks = smem + stage * C::kStageBytes, *vs = ks + C::kKBytes;
-                    const int n_tok = w.n - kPgTile * warp < kPgTile ? w.n - kPgTile * warp : kPgTile;
+                    const int n_tok = w.n - kPgTile * j < kPgTile ? w.n - kPgTile * j : kPgTile;
                     // 16-byte chunk c of token row r: 128-byte swizzle within each 64-entry half.
                     auto chunk = [&](const uint8_t *t, int r, int c) {
                         return t + (c >> 3) * C::kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
@@ -326,27 +335,30 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                             for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[nt][mt], a, qf[nt][kk][0], qf[nt][kk][1]);
                         }
                     }
-                    // ---- the tile's maximum and weights; tokens past the sequence weigh nothing
+                    // ---- running maximum, rescaled sums, weights; tokens past the sequence weigh nothing
                     uint32_t hi[NT][2][2], lo[NT][2][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float &x = s[nt][mt][e];
-                                x = 16 * mt + gid + 8 * (e >> 1) < n_tok ? __fmul_rn(x, p.scale_log2) : kNegInf;
-                                m[nt][e & 1] = fmaxf(m[nt][e & 1], x);
-                            }
+                        float f[2];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float v = m[nt][c];
+                            float v = kNegInf;
+#pragma unroll
+                            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    float &x = s[nt][mt][2 * r + c];
+                                    x = 16 * mt + gid + 8 * r < n_tok ? __fmul_rn(x, p.scale_log2) : kNegInf;
+                                    v = fmaxf(v, x);
+                                }
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                            m[nt][c] = v;
+                            v = fmaxf(v, m[nt][c]);
                             const float ref = v == kNegInf ? 0.0f : v;
-                            float sum = 0.0f;
+                            f[c] = ex2(m[nt][c] - ref);  // 0 at the first tile
+                            m[nt][c] = v;
+                            float sum = __fmul_rn(l[nt][c], f[c]);
 #pragma unroll
                             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -355,10 +367,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                                     x = ex2(x - ref);
                                     sum = __fadd_rn(sum, x);
                                 }
-                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 4));
-                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 8));
-                            sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 16));
                             l[nt][c] = sum;
+                        }
+                        if (j >= kPgGroupWarps) {
+#pragma unroll
+                            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[nt][mt][e] = __fmul_rn(o[nt][mt][e], f[e & 1]);
                         }
                         // Weights as two bf16 terms, turned so that tokens run along a thread's registers.
 #pragma unroll
@@ -397,21 +412,25 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     if (lane == 0) mbar_arrive(&empty[stage]);
                 }
             }
-            // ---- fold the tiles in order: heads 8 nt .. 8 nt + 7 at a time through shared memory
-            if (gid == 0) {
+            // ---- fold the warps in order: heads 8 nt .. 8 nt + 7 at a time through shared memory
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        red_m[warp][8 * nt + 2 * tig + c] = m[nt][c];
-                        red_l[warp][8 * nt + 2 * tig + c] = l[nt][c];
+                for (int c = 0; c < 2; ++c) {
+                    float v = l[nt][c];
+                    v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    if (gid == 0) {
+                        gm[cw][8 * nt + 2 * tig + c] = m[nt][c];
+                        gl[cw][8 * nt + 2 * tig + c] = v;
                     }
-            }
+                }
             const bool last = first[w.b + 1] - first[w.b] == 1;  // the sequence's only split
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int heads = p.G - 8 * nt < 8 ? p.G - 8 * nt : 8;
-                if (mine) {
+                if (cw < warps) {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -420,18 +439,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                             if (head < heads) so[head * C::kORow + d] = o[nt][mt][e];
                         }
                 }
-                pg_consumers_sync();
-                for (int i = tid; i < heads * (D / 4); i += 32 * kPgWarps) {
+                consumers_sync(1 + grp);
+                for (int i = ct; i < heads * (D / 4); i += 32 * kPgGroupWarps) {
                     const int hl = i / (D / 4), d = 4 * (i % (D / 4)), h = 8 * nt + hl;
-                    float mx = red_m[0][h];
-                    for (int t = 1; t < tiles; ++t) mx = fmaxf(mx, red_m[t][h]);
+                    float mx = gm[0][h];
+                    for (int t = 1; t < warps; ++t) mx = fmaxf(mx, gm[t][h]);
                     const float ref = mx == kNegInf ? 0.0f : mx;
                     float sum = 0.0f;
                     float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int t = 0; t < tiles; ++t) {
-                        const float f = ex2(red_m[t][h] - ref);
-                        const float4 v = *reinterpret_cast<const float4 *>(so_all + (t * 8 + hl) * C::kORow + d);
-                        sum = __fmaf_rn(red_l[t][h], f, sum);
+                    for (int t = 0; t < warps; ++t) {
+                        const float f = ex2(gm[t][h] - ref);
+                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * 8 + hl) * C::kORow + d);
+                        sum = __fmaf_rn(gl[t][h], f, sum);
                         r.x = __fmaf_rn(v.x, f, r.x);
                         r.y = __fmaf_rn(v.y, f, r.y);
                         r.z = __fmaf_rn(v.z, f, r.z);
@@ -448,7 +467,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         if (d == 0) p.part_ml[bh * p.S + w.split] = make_float2(mx, sum);
                     }
                 }
-                pg_consumers_sync();
+                consumers_sync(1 + grp);
             }
         }
     }

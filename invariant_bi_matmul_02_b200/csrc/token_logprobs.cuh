@@ -69,6 +69,11 @@ __device__ __forceinline__ TlTriple tl_merge(TlTriple a, TlTriple b, float c)
     return {m, __fadd_rn(__fmul_rn(fa, a.s), __fmul_rn(fb, b.s)), __fadd_rn(ta, tb)};
 }
 
+__device__ __forceinline__ float tl_logprob(float x, float m, float scale, float log_s)
+{
+    return __fsub_rn(__fmul_rn(x - m, scale), log_s);
+}
+
 // Ascending with the value; -0 as +0, NaN below everything.
 __device__ __forceinline__ uint32_t tl_order(float v)
 {
@@ -145,20 +150,42 @@ struct TlGroup {
     static constexpr int kSize = tl_group(BF16);
     uint32_t w[kTlWords];
 
-    // Elements e0 .. e0 + kSize - 1 of a row of V; elements past V are -inf.  VEC: rows are 16-byte aligned.
+    // Elements e0 .. e0 + kSize - 1 of a row of V; elements past V are -inf.  VEC: rows are 16-byte
+    // aligned.  Otherwise a group inside the row is cut out of the five aligned 16-byte pieces around it
+    // (all of them within the row), and the row's first and last groups are read by element.
     template <bool VEC>
     __device__ __forceinline__ void load(const void *row, int e0, int V)
     {
+        constexpr int kBytes = BF16 ? 2 : 4, kPer16 = 16 / kBytes;
+        const uint8_t *at = static_cast<const uint8_t *>(row) + (int64_t)e0 * kBytes;
         if (VEC && e0 + kSize <= V) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + (int64_t)e0 * (BF16 ? 2 : 4));
 #pragma unroll
-            for (int i = 0; i < kTlWords / 4; ++i) {
-                const uint4 v = __ldcs(src + i);
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
+            for (int i = 0; i < kTlWords / 4; ++i) put(i, __ldcs(reinterpret_cast<const uint4 *>(at) + i));
+            return;
+        }
+        if (!VEC && e0 > 0 && e0 + kSize + kPer16 <= V) {
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);  // the same for every group of the row
+            const uint4 *src = reinterpret_cast<const uint4 *>(at - off);
+            uint32_t x[kTlWords + 4];
+#pragma unroll
+            for (int i = 0; i < kTlWords / 4 + 1; ++i) {
+                const uint4 v = src[i];
+                x[4 * i] = v.x;
+                x[4 * i + 1] = v.y;
+                x[4 * i + 2] = v.z;
+                x[4 * i + 3] = v.w;
             }
+            if (off & 8u)
+#pragma unroll
+                for (int i = 0; i < kTlWords + 2; ++i) x[i] = x[i + 2];
+            if (off & 4u)
+#pragma unroll
+                for (int i = 0; i < kTlWords + 1; ++i) x[i] = x[i + 1];
+            if (BF16 && (off & 2u))
+#pragma unroll
+                for (int i = 0; i < kTlWords; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+#pragma unroll
+            for (int i = 0; i < kTlWords; ++i) w[i] = x[i];
             return;
         }
 #pragma unroll
@@ -171,6 +198,13 @@ struct TlGroup {
                 w[i] = e0 + i < V ? static_cast<const uint32_t *>(row)[e0 + i] : 0xff800000u;
             }
         }
+    }
+    __device__ __forceinline__ void put(int i, uint4 v)
+    {
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
     }
     __device__ __forceinline__ float2 pair(int i) const  // elements 2 i and 2 i + 1
     {
@@ -196,6 +230,77 @@ __device__ __forceinline__ float tl_element(const void *row, int e)
     return static_cast<const float *>(row)[e];
 }
 
+constexpr int kTlGroups = 128;  // candidate groups and elements the short way takes
+constexpr int kTlKeys = 256;
+
+struct TlScratch {
+    uint64_t keys[kTlKeys];
+    int32_t groups[kTlGroups];
+    int32_t n_groups, n_keys;
+};
+
+// The block's `top` best keys, in order, to out[] (places without an element: 0).  tl_max holds its `local`
+// pieces' group maxima, one column per thread.
+//   1. A bound that at least `top` groups reach: bisection over the ordered values of the threads' best
+//      groups, until no more than kTlGroups / 2 threads reach it (or it is exact).
+//   2. The groups that reach it are listed (more than one of a thread may), read again, and their elements
+//      that reach it listed: at least `top` elements do, so the best are among them.
+//   3. An element's place is the number of larger keys.
+// False when a list overflows: many equal values around the k-th.  All threads agree.
+template <bool BF16>
+__device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *row, int rank, int local,
+                                               const float *tl_max, TlScratch &s, uint64_t *out)
+{
+    constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto first = [&](int i) { return (i * p.cluster + rank) * kPiece + kGroup * tid; };  // of the thread's i-th group
+    uint32_t mine = 0;
+    for (int i = 0; i < local; ++i) {
+        const uint32_t o = first(i) < p.V ? tl_order(tl_max[i * kTlThreads + tid]) : 0u;
+        mine = o > mine ? o : mine;
+    }
+    // Invariant: at least `top` threads reach lo, fewer reach hi.  With fewer than `top` groups lo stays 0.
+    if (tid == 0) s.n_groups = s.n_keys = 0;
+    uint32_t lo = 0, hi = 0xffffffffu;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = __syncthreads_count(mine >= mid);
+        if (n >= p.top) lo = mid;
+        else hi = mid;
+        if (n >= p.top && n <= kTlGroups / 2) break;
+    }
+    __syncthreads();
+    for (int i = 0; i < local; ++i)
+        if (first(i) < p.V && tl_order(tl_max[i * kTlThreads + tid]) >= lo) {
+            const int at = atomicAdd(&s.n_groups, 1);
+            if (at < kTlGroups) s.groups[at] = first(i);
+        }
+    __syncthreads();
+    const int n_groups = s.n_groups;
+    if (n_groups > kTlGroups) return false;
+    for (int g = warp; g < n_groups; g += kTlWarps) {
+        const int e = s.groups[g] + lane;
+        if (lane < kGroup && e < p.V) {
+            const float v = tl_element<BF16>(row, e);
+            if (tl_order(v) >= lo) {
+                const int at = atomicAdd(&s.n_keys, 1);
+                if (at < kTlKeys) s.keys[at] = tl_key(v, (uint32_t)e);
+            }
+        }
+    }
+    if (tid < kTlMaxTop) out[tid] = 0;
+    __syncthreads();
+    const int n = s.n_keys;
+    if (n > kTlKeys) return false;
+    if (tid < n) {
+        const uint64_t key = s.keys[tid];
+        int place = 0;
+        for (int j = 0; j < n; ++j) place += s.keys[j] > key;
+        if (place < p.top) out[place] = key;
+    }
+    return true;
+}
+
 // Grid M * cluster blocks of kTlThreads; block r of a row's cluster takes pieces r, r + cluster, ...
 // Dynamic shared memory: the block's group maxima, kTlThreads floats per piece (top > 0 only).
 template <bool BF16, bool VEC>
@@ -206,6 +311,8 @@ __global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlP
     extern __shared__ float tl_max[];  // [pieces of this block][kTlThreads]
     __shared__ TlTriple triple[kTlMaxPieces * kTlWarps];
     __shared__ uint64_t best[kTlMaxCluster][kTlMaxTop];
+    __shared__ TlScratch scratch;
+    __shared__ float row_m, row_log_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)(blockIdx.x % (unsigned)p.cluster);
     const int64_t r = blockIdx.x / (unsigned)p.cluster;
@@ -255,70 +362,83 @@ __global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlP
     }
     __syncthreads();
 
-    // The block's best keys: warp 0 walks the group maxima in index order and reads again only the
-    // groups that beat the k-th key so far.
-    if (p.top > 0 && warp == 0) {
-        TlList list;
-        for (int i0 = 0; i0 < local * kTlThreads; i0 += 32) {
-            const int i = i0 + lane;
-            const int e0 = ((i / kTlThreads) * p.cluster + rank) * kPiece + kGroup * (i % kTlThreads);
-            const uint64_t gk = e0 < p.V ? tl_key(tl_max[i], (uint32_t)e0) : 0;
-            unsigned better = __ballot_sync(0xffffffffu, gk > list.kth);
-            while (better) {
-                const int src = __ffs(better) - 1;
-                const int e = __shfl_sync(0xffffffffu, e0, src) + lane;
-                list.offer(lane < kGroup && e < p.V ? tl_key(tl_element<BF16>(row, e), (uint32_t)e) : 0, p.top);
-                better &= better - 1;
-                better &= __ballot_sync(0xffffffffu, gk > list.kth);
+    if (p.top > 0) {
+        const bool found = tl_best_groups<BF16>(p, row, rank, local, tl_max, scratch, bests[rank]);
+        if (!found && warp == 0) {
+            // Too many groups or elements tie near the k-th: warp 0 walks the maxima in index order and reads
+            // again only the groups that beat the k-th key so far.
+            TlList list;
+            for (int i0 = 0; i0 < local * kTlThreads; i0 += 32) {
+                const int i = i0 + lane;
+                const int e0 = ((i / kTlThreads) * p.cluster + rank) * kPiece + kGroup * (i % kTlThreads);
+                const uint64_t gk = e0 < p.V ? tl_key(tl_max[i], (uint32_t)e0) : 0;
+                unsigned better = __ballot_sync(0xffffffffu, gk > list.kth);
+                while (better) {
+                    const int src = __ffs(better) - 1;
+                    const int e = __shfl_sync(0xffffffffu, e0, src) + lane;
+                    list.offer(lane < kGroup && e < p.V ? tl_key(tl_element<BF16>(row, e), (uint32_t)e) : 0, p.top);
+                    better &= better - 1;
+                    better &= __ballot_sync(0xffffffffu, gk > list.kth);
+                }
             }
+            bests[rank][lane] = list.mine;
         }
-        bests[rank][lane] = list.mine;
     }
     if (p.cluster > 1) {
         cluster_sync_all();
         if (rank != 0) return;
     } else {
-        __syncwarp();
+        __syncthreads();
     }
-    if (warp != 0) return;
 
-    TlTriple a{kNegInf, 0.0f, 0.0f};
-    for (int i = lane; i < p.pieces * kTlWarps; i += 32) a = tl_merge(a, triple[i], p.scale_log2);
+    // Warp 0 folds the triples; the block's upper half places the blocks' keys among one another.
+    uint64_t key = 0;
+    int place = 0;
+    if (warp == 0) {
+        TlTriple a{kNegInf, 0.0f, 0.0f};
+        for (int i = lane; i < p.pieces * kTlWarps; i += 32) a = tl_merge(a, triple[i], p.scale_log2);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const TlTriple b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                         __shfl_xor_sync(0xffffffffu, a.t, o)};
-        a = tl_merge(a, b, p.scale_log2);
-    }
-    // A row without a finite maximum has no distribution: all its values are NaN.
-    const float log_s = logf(a.s);
-    auto logprob = [&](float x) { return __fsub_rn(__fmul_rn(x - a.m, p.scale), log_s); };
-    if (lane == 0) {
-        if (p.logprobs != nullptr) {
-            const int32_t tok = p.tokens[r];
-            float v = 0.0f;  // a negative token: the row is not scored
-            if (tok >= p.V) {
-                *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
-                v = __int_as_float(0x7fffffff);
-            } else if (tok >= 0) {
-                v = logprob(tl_element<BF16>(row, tok));
+        for (int o = 16; o > 0; o >>= 1) {
+            const TlTriple b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                             __shfl_xor_sync(0xffffffffu, a.t, o)};
+            a = tl_merge(a, b, p.scale_log2);
+        }
+        // A row without a finite maximum has no distribution: all its values are NaN.
+        const float log_s = logf(a.s);
+        if (lane == 0) {
+            row_m = a.m;
+            row_log_s = log_s;
+            if (p.logprobs != nullptr) {
+                const int32_t tok = p.tokens[r];
+                float v = 0.0f;  // a negative token: the row is not scored
+                if (tok >= p.V) {
+                    *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                    v = __int_as_float(0x7fffffff);
+                } else if (tok >= 0) {
+                    v = tl_logprob(tl_element<BF16>(row, tok), a.m, p.scale, log_s);
+                }
+                p.logprobs[r] = v;
             }
-            p.logprobs[r] = v;
+            if (p.entropy != nullptr) p.entropy[r] = __fsub_rn(log_s, __fmul_rn(0.693147180559945309f, a.t / a.s));
+            if (p.logsumexp != nullptr) p.logsumexp[r] = __fmaf_rn(a.m, p.scale, log_s);
         }
-        if (p.entropy != nullptr) p.entropy[r] = __fsub_rn(log_s, __fmul_rn(0.693147180559945309f, a.t / a.s));
-        if (p.logsumexp != nullptr) p.logsumexp[r] = __fmaf_rn(a.m, p.scale, log_s);
+    } else if (tid >= kTlThreads / 2 && p.top > 0) {
+        // A key's place is the number of larger ones: its own list is in order (unused places hold 0).
+        const int q = (tid - kTlThreads / 2) >> 5;
+        place = lane;
+        if (q < p.cluster && lane < p.top) {
+            key = best[q][lane];
+            for (int o = 0; o < p.cluster; ++o)
+                if (o != q)
+#pragma unroll 4
+                    for (int j = 0; j < p.top; ++j) place += best[o][j] > key;
+        }
     }
-    if (p.top > 0) {
-        TlList list;
-        if (p.cluster > 1) {
-            for (int q = 0; q < p.cluster; ++q) list.offer(lane < p.top ? best[q][lane] : 0, p.top);
-        } else {
-            list.mine = best[0][lane];
-        }
-        if (lane < p.top) {
-            p.top_logprobs[r * p.top + lane] = logprob(tl_value((uint32_t)(list.mine >> 32)));
-            p.top_tokens[r * p.top + lane] = (int32_t)~(uint32_t)list.mine;
-        }
+    if (p.top == 0) return;
+    __syncthreads();
+    if (key != 0 && place < p.top) {
+        p.top_logprobs[r * p.top + place] = tl_logprob(tl_value((uint32_t)(key >> 32)), row_m, p.scale, row_log_s);
+        p.top_tokens[r * p.top + place] = (int32_t)~(uint32_t)key;
     }
 }
 
