@@ -14,7 +14,7 @@
 // numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
 // how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
 // other's arithmetic and loads.  The producer warp fills a ring of tiles (K and V of 32 tokens: 16 KB at
-// head size 128, 10 tiles; 8 KB at 64, 20 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
+// head size 128, 12 tiles; 8 KB at 64, 24 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
 // entries, each within one page and completing on the tile's mbarrier.  The lanes look the item's
 // pages up one item ahead and each issues the boxes of its own pages.
 //
@@ -40,7 +40,9 @@ constexpr int kPgWarps = 8;                      // consumer warps
 constexpr int kPgGroups = 2;                     // consumer groups, alternate items
 constexpr int kPgGroupWarps = kPgWarps / kPgGroups;
 constexpr int kPgSplit = 256;                    // tokens per split: two tiles for each warp of a group
-constexpr int kPgThreads = 32 * (kPgWarps + 1);  // the last warp produces
+constexpr int kPgProducers = 4;                  // producer warps
+constexpr int kPgThreads = 32 * (kPgWarps + kPgProducers);
+constexpr int kPgFold = 4;                       // query heads folded at a time
 constexpr int kPgSeqs = 2048;                    // sequences per launch (their prefix sums are in shared memory)
 
 template <int D>
@@ -49,9 +51,10 @@ struct PgShape {
     static constexpr int kHalfBytes = kPgTile * 128;        // one half of a tile's K or V
     static constexpr int kKBytes = kHalves * kHalfBytes;    // K (or V) of a tile
     static constexpr int kStageBytes = 2 * kKBytes;
-    static constexpr int kStages = 160 * 1024 / kStageBytes;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
     static constexpr int kORow = D + 4;                     // floats between heads of a warp's sums: no bank conflicts
-    static constexpr int kOBytes = kPgWarps * 8 * kORow * 4;
+    static constexpr int kOBytes = kPgWarps * kPgFold * kORow * 4;
+    static_assert(kStages % kPgProducers == 0, "a stage is always filled by the same producer warp");
     static constexpr int kSmem = kStages * kStageBytes + kOBytes + 1024;  // + alignment slack
 };
 
@@ -105,12 +108,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     using C = PgShape<D>;
     extern __shared__ uint8_t pg_raw[];
     uint8_t *smem = pg_raw + ((1024u - (smem_addr(pg_raw) & 1023u)) & 1023u);
-    float *so_all = reinterpret_cast<float *>(smem + C::kStages * C::kStageBytes);  // [warp][8 heads][kORow]
+    float *so_all = reinterpret_cast<float *>(smem + C::kStages * C::kStageBytes);  // [warp][kPgFold heads][kORow]
     __shared__ uint64_t full[C::kStages], empty[C::kStages];
     __shared__ float red_m[kPgWarps][8 * NT], red_l[kPgWarps][8 * NT];
     __shared__ int32_t first[kPgSeqs + 1];  // global number of each sequence's first split
     __shared__ int32_t lens_s[kPgSeqs];
-    __shared__ int32_t warp_total[kPgWarps + 1];
+    __shared__ int32_t warp_total[kPgThreads / 32];
     __shared__ int abort_flag_s;
     __shared__ int slot_use_s[C::kStages];  // uses of each stage that a consumer warp has passed
     volatile int *abort_flag = &abort_flag_s, *slot_use = slot_use_s;
@@ -172,8 +175,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         return {b, g, split, t0, left < kPgSplit ? left : kPgSplit};
     };
 
-    if (warp == kPgWarps) {
-        // ------------------------------------------------------------------ producer
+    if (warp >= kPgWarps) {
+        // ------------------------------------------------------------------ producers
+        // Tiles are numbered across the CTA's items; number n goes to stage n % kStages as its use n / kStages and
+        // is issued by producer warp n % kPgProducers.  kStages is a multiple of kPgProducers, so a stage's uses
+        // are issued by one warp in order, and its parity waits are exact.
+        const uint32_t pw = (uint32_t)(warp - kPgWarps);
         const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
         const int nb = kPgTile / p.box;                   // boxes per tile
         constexpr int kRegs = kPgSplit / 32;              // boxes of an item per lane, at one token a box
@@ -193,8 +200,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
             }
         };
-        uint32_t stage = 0, phase = 0;
-        int issued = 0;
+        uint32_t base = 0, mine = 0;  // the item's first tile number; tiles this warp has issued
         bool ok = true;
         Item w{};
         if (blockIdx.x < items) {
@@ -210,8 +216,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 look_up(wn, page_n, row_n);
             }
             const int boxes = (w.n + p.box - 1) / p.box, tiles = (w.n + kPgTile - 1) / kPgTile;
-            for (int j = 0; j < tiles; ++j) {
-                ok = __all_sync(0xffffffffu, wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status, lim));
+            for (int j = (int)((pw - base) % kPgProducers); j < tiles; j += kPgProducers) {
+                const uint32_t num = base + (uint32_t)j, stage = num % C::kStages, use = num / C::kStages;
+                ok = __all_sync(0xffffffffu, wait_bounded(&empty[stage], (use & 1u) ^ 1u, abort_flag, p.status, lim));
                 if (!ok) break;
                 const int k0 = j * nb, cnt = boxes - k0 < nb ? boxes - k0 : nb;
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(cnt * p.box * D * 2 * 2));
@@ -238,9 +245,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_4d(dst + C::kKBytes + h * C::kHalfBytes, &tm_v, &full[stage], 64 * h, c1, c2, pg, policy);
                 }
-                ++issued;
-                advance(stage, phase, C::kStages);
+                ++mine;
             }
+            base += (uint32_t)tiles;
             if (more) {
                 w = wn;
 #pragma unroll
@@ -251,11 +258,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             }
         }
         if (!ok && lane == 0) {
-            // A wait ran out: let every copy already issued land before shared memory goes away.
-            for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j) {
+            // A wait ran out: let every copy this warp has issued land before shared memory goes away.
+            constexpr uint32_t kOwn = C::kStages / kPgProducers;  // its stages
+            for (uint32_t i = mine > kOwn ? mine - kOwn : 0; i < mine; ++i) {
+                const uint32_t num = i * kPgProducers + pw, stage = num % C::kStages;
                 const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(smem_addr(&full[j % C::kStages]), (uint32_t)(j / C::kStages) & 1u) &&
-                       global_timer_ns() - t0 < lim) {
+                while (!mbar_try_wait(smem_addr(&full[stage]), (num / C::kStages) & 1u) && global_timer_ns() - t0 < lim) {
                 }
             }
         }
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int gid = lane >> 2, tig = lane & 3;
         uint32_t base = 0, local = 0;
         bool alive = true;
-        float *so_grp = so_all + grp * kPgGroupWarps * 8 * C::kORow, *so = so_grp + cw * 8 * C::kORow;
+        float *so_grp = so_all + grp * kPgGroupWarps * kPgFold * C::kORow, *so = so_grp + cw * kPgFold * C::kORow;
         float(*gm)[8 * NT] = red_m + grp * kPgGroupWarps, (*gl)[8 * NT] = red_l + grp * kPgGroupWarps;
         for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
             const Item w = item(it);
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     if (lane == 0) mbar_arrive(&empty[stage]);
                 }
             }
-            // ---- fold the warps in order: heads 8 nt .. 8 nt + 7 at a time through shared memory
+            // ---- fold the warps in order, kPgFold heads at a time through shared memory
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -428,20 +436,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
             const bool last = first[w.b + 1] - first[w.b] == 1;  // the sequence's only split
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int heads = p.G - 8 * nt < 8 ? p.G - 8 * nt : 8;
-                if (cw < warps) {
+            for (int round = 0; round < 8 * NT / kPgFold; ++round) {
+                const int h0 = kPgFold * round, nt = h0 / 8;
+                const int heads = p.G - h0 < kPgFold ? p.G - h0 : kPgFold;
+                if (heads <= 0) break;
+                const int hl = 8 * nt + 2 * tig - h0;  // this thread's heads are hl and hl + 1 of the round
+                if (cw < warps && hl >= 0 && hl < heads) {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int head = 2 * tig + (e & 1), d = 16 * mt + gid + 8 * (e >> 1);
-                            if (head < heads) so[head * C::kORow + d] = o[nt][mt][e];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (hl + (e & 1) < heads)
+                                so[(hl + (e & 1)) * C::kORow + 16 * mt + gid + 8 * (e >> 1)] = o[nt][mt][e];
                 }
                 consumers_sync(1 + grp);
                 for (int i = ct; i < heads * (D / 4); i += 32 * kPgGroupWarps) {
-                    const int hl = i / (D / 4), d = 4 * (i % (D / 4)), h = 8 * nt + hl;
+                    const int hl = i / (D / 4), d = 4 * (i % (D / 4)), h = h0 + hl;
                     float mx = gm[0][h];
                     for (int t = 1; t < warps; ++t) mx = fmaxf(mx, gm[t][h]);
                     const float ref = mx == kNegInf ? 0.0f : mx;
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     for (int t = 0; t < warps; ++t) {
                         const float f = ex2(gm[t][h] - ref);
-                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * 8 + hl) * C::kORow + d);
+                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * kPgFold + hl) * C::kORow + d);
                         sum = __fmaf_rn(gl[t][h], f, sum);
                         r.x = __fmaf_rn(v.x, f, r.x);
                         r.y = __fmaf_rn(v.y, f, r.y);
