@@ -522,28 +522,38 @@ inline bool strided_pieces(int64_t W, const void *p, int64_t s0, int64_t s1)
     return aligned16(p) && s0 % W == 0 && s1 % W == 0;
 }
 
-// Tokens per block of the rotation kernels: a few where that still leaves every SM several blocks (the
-// angles' latency is then shared), one otherwise.
-inline int rope_tokens(int64_t T, int sms) { return T >= (int64_t)4 * bi::kRopeTokens * sms ? bi::kRopeTokens : 1; }
+// Warps that share a token's heads in the rotation kernels: one where the tokens alone fill the GPU (the
+// angles are then worked out once per token), more for fewer tokens, as long as each has heads to take
+// (`steps`: head groups of a token).  Every head's arithmetic is the same.
+inline int rope_shares(int64_t T, int64_t steps, int sms)
+{
+    const int64_t want = ((int64_t)sms * 2 * bi::kRopeWarps + T - 1) / T;
+    return (int)(want < 1 ? 1 : want > steps ? steps : want);
+}
+inline int64_t rope_steps(int64_t H, int64_t D, int64_t R, int64_t W)
+{
+    const int64_t units = R / (2 * W) + (D - R) / W, heads = units < 32 ? 32 / units : 1;
+    return (H + heads - 1) / heads;
+}
 
 template <typename E, int W>
 bi_status launch_rope(const bi::RopeParams &p, bool half, int sms, cudaStream_t s)
 {
-    const int tokens = rope_tokens(p.T, sms);
-    const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(bi::kRopeThreads);
-    const size_t smem = (size_t)tokens * (p.R / 2) * sizeof(float2);
-    return half ? launch_pdl(bi::rope_kernel<E, W, true>, grid, block, smem, s, p, tokens)
-                : launch_pdl(bi::rope_kernel<E, W, false>, grid, block, smem, s, p, tokens);
+    const int shares = rope_shares(p.T, rope_steps(p.H, p.D, p.R, W), sms);
+    const dim3 grid((unsigned)((p.T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps)), block(bi::kRopeThreads);
+    const size_t smem = (size_t)bi::kRopeWarps * (p.R / 2) * sizeof(float2);
+    return half ? launch_pdl(bi::rope_kernel<E, W, true>, grid, block, smem, s, p, shares)
+                : launch_pdl(bi::rope_kernel<E, W, false>, grid, block, smem, s, p, shares);
 }
 
 template <int W>
 bi_status launch_append(const bi::AppendParams &p, bool half, int sms, cudaStream_t s)
 {
-    const int tokens = rope_tokens(p.T, sms);
-    const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(bi::kRopeThreads);
-    const size_t smem = (size_t)tokens * (p.R / 2) * sizeof(float2);
-    return half ? launch_pdl(bi::paged_append_kernel<W, true>, grid, block, smem, s, p, tokens)
-                : launch_pdl(bi::paged_append_kernel<W, false>, grid, block, smem, s, p, tokens);
+    const int shares = rope_shares(p.T, rope_steps((p.q ? p.Hq : 0) + p.Hkv, p.D, p.R, W), sms);
+    const dim3 grid((unsigned)((p.T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps)), block(bi::kRopeThreads);
+    const size_t smem = (size_t)bi::kRopeWarps * (p.R / 2) * sizeof(float2);
+    return half ? launch_pdl(bi::paged_append_kernel<W, true>, grid, block, smem, s, p, shares)
+                : launch_pdl(bi::paged_append_kernel<W, false>, grid, block, smem, s, p, shares);
 }
 
 // A cache description that the paged entry points take.

@@ -8,11 +8,12 @@
 // each output is one fp32 expression rounded once.  The work is elementwise, so every launch shape
 // gives the same bits.
 //
-// Bound by memory for many tokens and by latency for few.  A block takes a few tokens, so that each
-// token's R/2 sines and cosines are computed once and read from shared memory by every head.  A
-// thread's unit is W entries a and their W partners b (16-byte pieces where sizes, strides and
-// addresses allow it, single entries otherwise; the arithmetic is the same), and it has the first
-// units' loads in flight before the angles are worked out.
+// Bound by memory for many tokens and by latency for few.  A warp takes a token (or a share of its heads
+// where there are few tokens): it works out the token's R/2 sines and cosines once, into its own piece of
+// shared memory, and its lanes keep a fixed place in the head while they walk the heads.  A lane's unit
+// is W entries a and their W partners b (16-byte pieces where sizes, strides and addresses allow it, single
+// entries otherwise; the arithmetic is the same), and kRopeUnits heads' loads are in flight before
+// the first angle is needed.
 #pragma once
 
 #include <cstdint>
@@ -24,9 +25,9 @@
 namespace bi {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;    // tokens per block when there are many
-constexpr int kRopeMaxDim = 1024; // head size limit: kRopeTokens * D/2 cosines and sines are 16 KB
-constexpr int kRopeUnits = 4;     // units a thread has in flight
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 32 KB
+constexpr int kRopeUnits = 4;      // heads a lane has in flight
 
 // W consecutive entries (16 bytes for W > 1) as they sit in memory.
 template <typename E, int W>
@@ -71,12 +72,23 @@ __device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const 
     }
 }
 
-// Where a unit's entries sit in its head.  Units 0 .. R/2W-1 are pairs, the rest copies of one piece.
+// A lane's place in the heads its warp walks.  A head has R/2W units of pairs and then (D - R)/W single
+// pieces that are copied; 32 / units heads are taken at a time (or one head 32 units at a time).
 template <int W, bool HALF>
-struct RopeUnit {
-    int a, b;   // entry offsets of the two pieces (b < 0: one piece, copied)
-    int pair;   // first pair number
-    __device__ __forceinline__ RopeUnit(int u, int R)
+struct RopeLane {
+    int units, heads;  // units per head; heads the warp takes at a time
+    int head, unit;    // this lane's first head and unit (unit >= units: the lane idles)
+    __device__ __forceinline__ RopeLane(int D, int R)
+    {
+        const int lane = threadIdx.x & 31;
+        units = R / (2 * W) + (D - R) / W;
+        heads = units < 32 ? 32 / units : 1;
+        head = units < 32 ? lane / units : 0;
+        unit = lane - head * units;
+        if (head >= heads) unit = units;
+    }
+    // Entry offsets of unit u's two pieces (b < 0: one piece, copied) and its first pair.
+    static __device__ __forceinline__ void place(int u, int R, int &a, int &b, int &pair)
     {
         const int np = R / (2 * W);
         if (u < np) {
@@ -91,6 +103,13 @@ struct RopeUnit {
     }
 };
 
+// The warp's token's cosines and sines into cs[R/2].
+__device__ __forceinline__ void rope_angles(float2 *cs, const double *inv_freq, int half, int32_t pos, float scale, bool inverse)
+{
+    for (int i = threadIdx.x & 31; i < half; i += 32) cs[i] = rope_angle(pos, inv_freq[i], scale, inverse);
+    __syncwarp();
+}
+
 struct RopeParams {
     const void *x;
     void *y;
@@ -103,54 +122,57 @@ struct RopeParams {
     int32_t inverse;
 };
 
+// `shares` warps take a token's heads in turn.
 template <typename E, int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int tokens)
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int shares)
 {
-    extern __shared__ float2 rope_cs[];  // [tokens][R/2]
-    const int tid = threadIdx.x, half = p.R / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * tokens;
-    const int nt = (int)(p.T - t0 < tokens ? p.T - t0 : tokens);
-    const int per_head = p.R / (2 * W) + (p.D - p.R) / W;
-    const int per_token = per_head * p.H, units = per_token * nt;
-    const E *x = static_cast<const E *>(p.x) + t0 * p.x_token;
-    E *y = static_cast<E *>(p.y) + t0 * p.y_token;
-    const bool in_place = p.x == p.y;
+    extern __shared__ float2 rope_cs[];  // [kRopeWarps][R/2]
+    const int half = p.R / 2;
+    float2 *cs = rope_cs + (threadIdx.x >> 5) * half;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
-
-    Piece<E, W> a[kRopeUnits], b[kRopeUnits];
-    for (int u0 = tid; u0 - tid < units; u0 += kRopeUnits * kRopeThreads) {
+    if (t >= p.T) return;
+    const RopeLane<W, HALF> me(p.D, p.R);
+    const int h_first = me.head + (int)(gw - t * shares) * me.heads, h_step = me.heads * shares;
+    const E *x = static_cast<const E *>(p.x) + t * p.x_token;
+    E *y = static_cast<E *>(p.y) + t * p.y_token;
+    const bool in_place = p.x == p.y;
+    bool ready = false;
+    for (int u0 = 0; u0 < me.units; u0 += 32) {
+        const int u = me.unit + u0;
+        const bool on = u < me.units;
+        int ea, eb, pair;
+        RopeLane<W, HALF>::place(u, p.R, ea, eb, pair);
+        for (int h0 = h_first; h0 - me.head < p.H; h0 += kRopeUnits * h_step) {
+            Piece<E, W> a[kRopeUnits], b[kRopeUnits];
 #pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
-            const int u = u0 + k * kRopeThreads;
-            if (u < units) {
-                const int t = u / per_token, r = u - t * per_token, h = r / per_head;
-                const RopeUnit<W, HALF> w(r - h * per_head, p.R);
-                const E *src = x + t * p.x_token + h * p.x_head;
-                a[k] = *reinterpret_cast<const Piece<E, W> *>(src + w.a);
-                if (w.b >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + w.b);
+            for (int k = 0; k < kRopeUnits; ++k) {
+                const int h = h0 + k * h_step;
+                if (on && h < p.H) {
+                    const E *src = x + h * p.x_head;
+                    a[k] = *reinterpret_cast<const Piece<E, W> *>(src + ea);
+                    if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + eb);
+                }
             }
-        }
-        if (u0 == tid) {  // the first units' loads are in flight
-            for (int i = tid; i < nt * half; i += kRopeThreads) {
-                const int t = i / half;
-                rope_cs[i] = rope_angle(p.pos[t0 + t], p.inv_freq[i - t * half], p.scale, p.inverse != 0);
+            if (!ready) {  // the first loads are in flight
+                if (half > 0) rope_angles(cs, p.inv_freq, half, p.pos[t], p.scale, p.inverse != 0);
+                ready = true;
             }
-            __syncthreads();
-        }
+            float2 c[W];
+            if (on && eb >= 0)
 #pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
-            const int u = u0 + k * kRopeThreads;
-            if (u < units) {
-                const int t = u / per_token, r = u - t * per_token, h = r / per_head;
-                const RopeUnit<W, HALF> w(r - h * per_head, p.R);
-                E *dst = y + t * p.y_token + h * p.y_head;
-                if (w.b >= 0) {
-                    rope_unit<E, W, HALF>(a[k], b[k], rope_cs + t * half + w.pair);
-                    *reinterpret_cast<Piece<E, W> *>(dst + w.a) = a[k];
-                    *reinterpret_cast<Piece<E, W> *>(dst + w.b) = b[k];
-                } else if (!in_place) {
-                    *reinterpret_cast<Piece<E, W> *>(dst + w.a) = a[k];
+                for (int j = 0; j < W; ++j) c[j] = cs[pair + j];
+#pragma unroll
+            for (int k = 0; k < kRopeUnits; ++k) {
+                const int h = h0 + k * h_step;
+                if (on && h < p.H) {
+                    E *dst = y + h * p.y_head;
+                    if (eb >= 0) {
+                        rope_unit<E, W, HALF>(a[k], b[k], c);
+                        *reinterpret_cast<Piece<E, W> *>(dst + eb) = b[k];
+                    }
+                    if (eb >= 0 || !in_place) *reinterpret_cast<Piece<E, W> *>(dst + ea) = a[k];
                 }
             }
         }
@@ -220,80 +242,83 @@ __device__ __forceinline__ AppendSlot append_slot(const AppendParams &p, int64_t
     return {page * p.c_page + (at % p.page_size) * p.c_token, p.positions ? p.positions[t] : (int32_t)at};
 }
 
+// `shares` warps take a token's query and key heads, and then its values, in turn.
 template <int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const AppendParams p, int tokens)
+__global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const AppendParams p, int shares)
 {
     using E = __nv_bfloat16;
-    extern __shared__ float2 rope_cs[];  // [tokens][R/2]
-    __shared__ AppendSlot slot[kRopeTokens];
-    const int tid = threadIdx.x, half = p.R / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * tokens;
-    const int nt = (int)(p.T - t0 < tokens ? p.T - t0 : tokens);
-    const int per_head = p.R / (2 * W) + (p.D - p.R) / W, per_v = p.D / W;
-    const int hq = p.q ? p.Hq : 0, turned = per_head * (hq + p.Hkv);
-    const int per_token = turned + per_v * p.Hkv, units = per_token * nt;
+    extern __shared__ float2 rope_cs[];  // [kRopeWarps][R/2]
+    const int half = p.R / 2, lane = threadIdx.x & 31;
+    float2 *cs = rope_cs + (threadIdx.x >> 5) * half;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
-
-    // Unit u: a piece (or pair of pieces) of a query head, a key head or a value head of token t.
-    struct At {
-        int t, head, a, b, pair;
-        int kind;  // 0 query, 1 key, 2 value
-    };
-    auto locate = [&](int u) -> At {
-        const int t = u / per_token, r = u - t * per_token;
-        if (r >= turned) {
-            const int w = r - turned, h = w / per_v;
-            return {t, h, (w - h * per_v) * W, -1, 0, 2};
-        }
-        const int h = r / per_head;
-        const RopeUnit<W, HALF> w(r - h * per_head, p.R);
-        return {t, h < hq ? h : h - hq, w.a, w.b, w.pair, h < hq ? 0 : 1};
-    };
-
-    Piece<E, W> a[kRopeUnits], b[kRopeUnits];
-    for (int u0 = tid; u0 - tid < units; u0 += kRopeUnits * kRopeThreads) {
+    if (t >= p.T) return;
+    const int share = (int)(gw - t * shares);
+    const RopeLane<W, HALF> me(p.D, p.R);
+    const int hq = p.q ? p.Hq : 0, H = hq + p.Hkv;  // heads 0 .. hq-1 query, then key
+    const int h_first = me.head + share * me.heads, h_step = me.heads * shares;
+    const E *q = p.q + t * p.q_token, *kk = p.k + t * p.k_token, *vv = p.v + t * p.v_token;
+    E *qo = p.q_out + t * p.qo_token;
+    AppendSlot slot{-1, 0};
+    bool ready = false;
+    for (int u0 = 0; u0 < me.units; u0 += 32) {
+        const int u = me.unit + u0;
+        const bool on = u < me.units;
+        int ea, eb, pair;
+        RopeLane<W, HALF>::place(u, p.R, ea, eb, pair);
+        for (int h0 = h_first; h0 - me.head < H; h0 += kRopeUnits * h_step) {
+            Piece<E, W> a[kRopeUnits], b[kRopeUnits];
 #pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
-            const int u = u0 + k * kRopeThreads;
-            if (u < units) {
-                const At w = locate(u);
-                const int64_t t = t0 + w.t;
-                const E *src = w.kind == 0   ? p.q + t * p.q_token + w.head * p.q_head
-                               : w.kind == 1 ? p.k + t * p.k_token + w.head * p.k_head
-                                             : p.v + t * p.v_token + w.head * p.v_head;
-                a[k] = *reinterpret_cast<const Piece<E, W> *>(src + w.a);
-                if (w.b >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + w.b);
-            }
-        }
-        if (u0 == tid) {  // the first units' loads are in flight
-            if ((tid >> 5) < nt) {
-                const AppendSlot s = append_slot(p, t0 + (tid >> 5));
-                if ((tid & 31) == 0) slot[tid >> 5] = s;
-            }
-            __syncthreads();
-            for (int i = tid; i < nt * half; i += kRopeThreads) {
-                const int t = i / half;
-                rope_cs[i] = rope_angle(slot[t].pos, p.inv_freq[i - t * half], p.scale, false);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
-            const int u = u0 + k * kRopeThreads;
-            if (u < units) {
-                const At w = locate(u);
-                const int64_t t = t0 + w.t, row = slot[w.t].cache;
-                if (row < 0) continue;
-                E *dst = w.kind == 0   ? p.q_out + t * p.qo_token + w.head * p.qo_head
-                         : w.kind == 1 ? p.k_cache + row + w.head * p.c_head
-                                       : p.v_cache + row + w.head * p.c_head;
-                if (w.b >= 0) {
-                    rope_unit<E, W, HALF>(a[k], b[k], rope_cs + w.t * half + w.pair);
-                    *reinterpret_cast<Piece<E, W> *>(dst + w.b) = b[k];
+            for (int k = 0; k < kRopeUnits; ++k) {
+                const int h = h0 + k * h_step;
+                if (on && h < H) {
+                    const E *src = h < hq ? q + h * p.q_head : kk + (h - hq) * p.k_head;
+                    a[k] = *reinterpret_cast<const Piece<E, W> *>(src + ea);
+                    if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + eb);
                 }
-                *reinterpret_cast<Piece<E, W> *>(dst + w.a) = a[k];
             }
+            if (!ready) {  // the first loads are in flight
+                slot = append_slot(p, t);
+                if (slot.cache < 0) return;
+                if (half > 0) rope_angles(cs, p.inv_freq, half, slot.pos, p.scale, false);
+                ready = true;
+            }
+            float2 c[W];
+            if (on && eb >= 0)
+#pragma unroll
+                for (int j = 0; j < W; ++j) c[j] = cs[pair + j];
+#pragma unroll
+            for (int k = 0; k < kRopeUnits; ++k) {
+                const int h = h0 + k * h_step;
+                if (on && h < H) {
+                    E *dst = h < hq ? qo + h * p.qo_head : p.k_cache + slot.cache + (h - hq) * p.c_head;
+                    if (eb >= 0) {
+                        rope_unit<E, W, HALF>(a[k], b[k], c);
+                        *reinterpret_cast<Piece<E, W> *>(dst + eb) = b[k];
+                    }
+                    *reinterpret_cast<Piece<E, W> *>(dst + ea) = a[k];
+                }
+            }
+        }
+    }
+    if (!ready) {  // a share without a head
+        slot = append_slot(p, t);
+        if (slot.cache < 0) return;
+    }
+    const int per_v = p.D / W, pieces = per_v * p.Hkv;
+    for (int i0 = share * 32 + lane; i0 - lane < pieces; i0 += kRopeUnits * 32 * shares) {
+        Piece<E, W> a[kRopeUnits];
+#pragma unroll
+        for (int k = 0; k < kRopeUnits; ++k) {
+            const int i = i0 + k * 32 * shares, h = i / per_v;
+            if (i < pieces) a[k] = *reinterpret_cast<const Piece<E, W> *>(vv + h * p.v_head + (i - h * per_v) * W);
+        }
+#pragma unroll
+        for (int k = 0; k < kRopeUnits; ++k) {
+            const int i = i0 + k * 32 * shares, h = i / per_v;
+            if (i < pieces)
+                *reinterpret_cast<Piece<E, W> *>(p.v_cache + slot.cache + h * p.c_head + (i - h * per_v) * W) = a[k];
         }
     }
 }
