@@ -527,7 +527,7 @@ inline bool strided_pieces(int64_t W, const void *p, int64_t s0, int64_t s1)
 // (`steps`: head groups of a token).  Every head's arithmetic is the same.
 inline int rope_shares(int64_t T, int64_t steps, int sms)
 {
-    const int64_t want = ((int64_t)sms * 2 * bi::kRopeWarps + T - 1) / T;
+    const int64_t want = ((int64_t)sms * 16 + T - 1) / T;  // 16 warps an SM
     return (int)(want < 1 ? 1 : want > steps ? steps : want);
 }
 inline int64_t rope_steps(int64_t H, int64_t D, int64_t R, int64_t W)

@@ -24,15 +24,21 @@
 
 namespace bi {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBlocks = 6;      // resident per SM, a bound on registers
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 32 KB
-constexpr int kRopeUnits = 4;      // heads a lane has in flight
+constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 16 KB
+constexpr int kRopeUnits = 2;      // a lane's buffers: one head is turned while the others are on their way
+constexpr int kRopeCopies = 4;     // value pieces a lane has in flight
 
-// W consecutive entries (16 bytes for W > 1) as they sit in memory.
+// W consecutive entries as they sit in memory: 16 bytes, or one entry (W = 1).
 template <typename E, int W>
-struct alignas(W * sizeof(E)) Piece {
-    E e[W];
+struct alignas(16) Piece {
+    uint32_t w[4];
+};
+template <typename E>
+struct Piece<E, 1> {
+    E e;
 };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -40,35 +46,81 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float v, float &o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
 
-// (cos, sin) of pos * inv_freq, times scale.
-__device__ __forceinline__ float2 rope_angle(int32_t pos, double inv_freq, float scale, bool inverse)
+// Cosine and sine of pos * inv_freq, times scale.
+__device__ __forceinline__ void rope_angle(int32_t pos, double inv_freq, float scale, bool inverse, float &c, float &s)
 {
     const double turns = (double)pos * (inv_freq * 0.15915494309189533576888);
     const float f = (float)(turns - rint(turns));  // in [-1/2, 1/2]
-    float s, c;
     sincospif(2.0f * f, &s, &c);
     if (inverse) s = -s;
-    return make_float2(__fmul_rn(c, scale), __fmul_rn(s, scale));
+    c = __fmul_rn(c, scale);
+    s = __fmul_rn(s, scale);
 }
 
-// Rotates the pairs of one unit.  HALF: a holds entries i .. i+W-1 and b their partners
-// i + R/2 ..; otherwise a and b are 2W consecutive entries, pairs side by side.
-template <typename E, int W, bool HALF>
-__device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const float2 *cs)
-{
+// The cosines, sines and negated sines of a unit's W pairs.
+template <int W>
+struct RopeTurn {
+    float c[W], s[W], n[W];
+    __device__ __forceinline__ void load(const float *cs, int half, int pair)
+    {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        E *pa, *pb;
-        if (HALF) {
-            pa = &a.e[j];
-            pb = &b.e[j];
-        } else {
-            pa = 2 * j < W ? &a.e[2 * j] : &b.e[2 * j - W];
-            pb = 2 * j + 1 < W ? &a.e[2 * j + 1] : &b.e[2 * j + 1 - W];
+        for (int j = 0; j < W; ++j) {
+            c[j] = cs[pair + j];
+            s[j] = cs[half + pair + j];
+            n[j] = -s[j];
         }
-        const float x = to_f32(*pa), y = to_f32(*pb), c = cs[j].x, s = cs[j].y;
-        from_f32(__fmaf_rn(x, c, -__fmul_rn(y, s)), *pa);
-        from_f32(__fmaf_rn(y, c, __fmul_rn(x, s)), *pb);
+    }
+    // Pairs j and j + 1: (x, y) to (x c - y s, y c + x s), each one product and one fused sum.
+    __device__ __forceinline__ void turn2(int j, uint64_t &x, uint64_t &y) const
+    {
+        const uint64_t c2 = f2_pack(c[j], c[j + 1]);
+        const uint64_t u = f2_fma(x, c2, f2_mul(y, f2_pack(n[j], n[j + 1])));
+        y = f2_fma(y, c2, f2_mul(x, f2_pack(s[j], s[j + 1])));
+        x = u;
+    }
+};
+
+// Rotates the W pairs of one unit in place.  HALF: a holds entries i .. i+W-1 and b their partners i + R/2 ..;
+// otherwise a and b are 2W consecutive entries, pairs side by side.
+template <typename E, int W, bool HALF>
+__device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const RopeTurn<W> &t)
+{
+    if constexpr (W == 1) {
+        const float x = to_f32(a.e), y = to_f32(b.e);
+        from_f32(__fmaf_rn(x, t.c[0], __fmul_rn(y, t.n[0])), a.e);
+        from_f32(__fmaf_rn(y, t.c[0], __fmul_rn(x, t.s[0])), b.e);
+    } else if constexpr (W == 8 && HALF) {  // bf16: a word holds entries 2j and 2j + 1
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint64_t x = f2_pack(bf16lo(a.w[j]), bf16hi(a.w[j])), y = f2_pack(bf16lo(b.w[j]), bf16hi(b.w[j]));
+            t.turn2(2 * j, x, y);
+            const float2 u = f2_unpack(x), v = f2_unpack(y);
+            a.w[j] = pack_bf16x2(u.x, u.y);
+            b.w[j] = pack_bf16x2(v.x, v.y);
+        }
+    } else if constexpr (W == 8) {  // bf16: a word holds a pair
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t &w0 = j < 4 ? a.w[j] : b.w[j - 4], &w1 = j < 4 ? a.w[j + 1] : b.w[j - 3];
+            uint64_t x = f2_pack(bf16lo(w0), bf16lo(w1)), y = f2_pack(bf16hi(w0), bf16hi(w1));
+            t.turn2(j, x, y);
+            const float2 u = f2_unpack(x), v = f2_unpack(y);
+            w0 = pack_bf16x2(u.x, v.x);
+            w1 = pack_bf16x2(u.y, v.y);
+        }
+    } else {  // fp32: four entries a piece
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            uint32_t &x0 = HALF ? a.w[j] : j == 0 ? a.w[0] : b.w[0], &x1 = HALF ? a.w[j + 1] : j == 0 ? a.w[2] : b.w[2];
+            uint32_t &y0 = HALF ? b.w[j] : j == 0 ? a.w[1] : b.w[1], &y1 = HALF ? b.w[j + 1] : j == 0 ? a.w[3] : b.w[3];
+            uint64_t x = f2_pack(__uint_as_float(x0), __uint_as_float(x1)), y = f2_pack(__uint_as_float(y0), __uint_as_float(y1));
+            t.turn2(j, x, y);
+            const float2 u = f2_unpack(x), v = f2_unpack(y);
+            x0 = __float_as_uint(u.x);
+            x1 = __float_as_uint(u.y);
+            y0 = __float_as_uint(v.x);
+            y1 = __float_as_uint(v.y);
+        }
     }
 }
 
@@ -103,11 +155,66 @@ struct RopeLane {
     }
 };
 
-// The warp's token's cosines and sines into cs[R/2].
-__device__ __forceinline__ void rope_angles(float2 *cs, const double *inv_freq, int half, int32_t pos, float scale, bool inverse)
+// The warp's token's R/2 cosines, then R/2 sines, into cs.
+__device__ __forceinline__ void rope_angles(float *cs, const double *inv_freq, int half, int32_t pos, float scale, bool inverse)
 {
-    for (int i = threadIdx.x & 31; i < half; i += 32) cs[i] = rope_angle(pos, inv_freq[i], scale, inverse);
+    for (int i = threadIdx.x & 31; i < half; i += 32) rope_angle(pos, inv_freq[i], scale, inverse, cs[i], cs[half + i]);
     __syncwarp();
+}
+
+// Walks heads 0 .. H-1 of one token, every `shares`-th group of them from group `group` on: src to the
+// place that dst() gives.  ready() is called once the first loads are in flight and before cs or dst() is
+// needed; false ends the walk.  copy: whether single pieces are written (not when y is x).
+template <typename E, int W, bool HALF, typename Ready, typename Dst>
+__device__ __forceinline__ bool rope_walk(const RopeLane<W, HALF> &me, const E *src, int64_t src_head, int64_t dst_head,
+                                          int H, int R, int group, int shares, const float *cs, bool copy, Ready ready,
+                                          Dst dst)
+{
+    const int h_step = me.heads * shares, half = R / 2;
+    const int64_t src_step = h_step * src_head, dst_step = h_step * dst_head;
+    for (int u0 = 0; u0 < me.units; u0 += 32) {
+        const int u = me.unit + u0;
+        const bool on = u < me.units;
+        int ea, eb, pair;
+        RopeLane<W, HALF>::place(u, R, ea, eb, pair);
+        // Heads left for this lane and for the warp's first lane (the loop's bound).
+        const int h = me.head + group * me.heads;
+        int left = on && h < H ? (H - h + h_step - 1) / h_step : 0;
+        int turns = group * me.heads < H ? (H - group * me.heads + h_step - 1) / h_step : 0;
+        if (turns == 0) continue;
+        const E *from = src + h * src_head;
+        Piece<E, W> a[kRopeUnits], b[kRopeUnits];
+        auto load = [&](int k, bool some) {
+            if (some) {
+                a[k] = *reinterpret_cast<const Piece<E, W> *>(from + ea);
+                if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(from + eb);
+            }
+            from += src_step;
+        };
+#pragma unroll
+        for (int k = 0; k + 1 < kRopeUnits; ++k) load(k, left > k);
+        if (!ready()) return false;
+        RopeTurn<W> turn;
+        if (on && eb >= 0) turn.load(cs, half, pair);
+        E *to = dst() + h * dst_head;
+        while (turns > 0) {
+#pragma unroll
+            for (int k = 0; k < kRopeUnits; ++k) {
+                load((k + kRopeUnits - 1) % kRopeUnits, left > kRopeUnits - 1);
+                if (left > 0) {
+                    if (eb >= 0) {
+                        rope_unit<E, W, HALF>(a[k], b[k], turn);
+                        *reinterpret_cast<Piece<E, W> *>(to + eb) = b[k];
+                    }
+                    if (eb >= 0 || copy) *reinterpret_cast<Piece<E, W> *>(to + ea) = a[k];
+                }
+                to += dst_step;
+                --left;
+                if (--turns == 0) break;
+            }
+        }
+    }
+    return true;
 }
 
 struct RopeParams {
@@ -124,59 +231,25 @@ struct RopeParams {
 
 // `shares` warps take a token's heads in turn.
 template <typename E, int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int shares)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p, int shares)
 {
-    extern __shared__ float2 rope_cs[];  // [kRopeWarps][R/2]
-    const int half = p.R / 2;
-    float2 *cs = rope_cs + (threadIdx.x >> 5) * half;
+    extern __shared__ __align__(16) float rope_cs[];  // [kRopeWarps][R]
+    float *cs = rope_cs + (threadIdx.x >> 5) * p.R;
     const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
     const RopeLane<W, HALF> me(p.D, p.R);
-    const int h_first = me.head + (int)(gw - t * shares) * me.heads, h_step = me.heads * shares;
-    const E *x = static_cast<const E *>(p.x) + t * p.x_token;
-    E *y = static_cast<E *>(p.y) + t * p.y_token;
-    const bool in_place = p.x == p.y;
-    bool ready = false;
-    for (int u0 = 0; u0 < me.units; u0 += 32) {
-        const int u = me.unit + u0;
-        const bool on = u < me.units;
-        int ea, eb, pair;
-        RopeLane<W, HALF>::place(u, p.R, ea, eb, pair);
-        for (int h0 = h_first; h0 - me.head < p.H; h0 += kRopeUnits * h_step) {
-            Piece<E, W> a[kRopeUnits], b[kRopeUnits];
-#pragma unroll
-            for (int k = 0; k < kRopeUnits; ++k) {
-                const int h = h0 + k * h_step;
-                if (on && h < p.H) {
-                    const E *src = x + h * p.x_head;
-                    a[k] = *reinterpret_cast<const Piece<E, W> *>(src + ea);
-                    if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + eb);
-                }
-            }
-            if (!ready) {  // the first loads are in flight
-                if (half > 0) rope_angles(cs, p.inv_freq, half, p.pos[t], p.scale, p.inverse != 0);
-                ready = true;
-            }
-            float2 c[W];
-            if (on && eb >= 0)
-#pragma unroll
-                for (int j = 0; j < W; ++j) c[j] = cs[pair + j];
-#pragma unroll
-            for (int k = 0; k < kRopeUnits; ++k) {
-                const int h = h0 + k * h_step;
-                if (on && h < p.H) {
-                    E *dst = y + h * p.y_head;
-                    if (eb >= 0) {
-                        rope_unit<E, W, HALF>(a[k], b[k], c);
-                        *reinterpret_cast<Piece<E, W> *>(dst + eb) = b[k];
-                    }
-                    if (eb >= 0 || !in_place) *reinterpret_cast<Piece<E, W> *>(dst + ea) = a[k];
-                }
-            }
-        }
-    }
+    bool have = false;
+    rope_walk<E, W, HALF>(
+        me, static_cast<const E *>(p.x) + t * p.x_token, p.x_head, p.y_head, p.H, p.R, (int)(gw - t * shares), shares, cs,
+        p.x != p.y,
+        [&] {
+            if (!have && p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
+            have = true;
+            return true;
+        },
+        [&] { return static_cast<E *>(p.y) + t * p.y_token; });
 }
 
 // ------------------------------------------------------------------------------- paged append
@@ -242,80 +315,53 @@ __device__ __forceinline__ AppendSlot append_slot(const AppendParams &p, int64_t
     return {page * p.c_page + (at % p.page_size) * p.c_token, p.positions ? p.positions[t] : (int32_t)at};
 }
 
-// `shares` warps take a token's query and key heads, and then its values, in turn.
+// `shares` warps take a token's query heads, key heads and values in turn.
 template <int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const AppendParams p, int shares)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel(const AppendParams p, int shares)
 {
     using E = __nv_bfloat16;
-    extern __shared__ float2 rope_cs[];  // [kRopeWarps][R/2]
-    const int half = p.R / 2, lane = threadIdx.x & 31;
-    float2 *cs = rope_cs + (threadIdx.x >> 5) * half;
+    extern __shared__ __align__(16) float rope_cs[];  // [kRopeWarps][R]
+    const int lane = threadIdx.x & 31;
+    float *cs = rope_cs + (threadIdx.x >> 5) * p.R;
     const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
     const int share = (int)(gw - t * shares);
     const RopeLane<W, HALF> me(p.D, p.R);
-    const int hq = p.q ? p.Hq : 0, H = hq + p.Hkv;  // heads 0 .. hq-1 query, then key
-    const int h_first = me.head + share * me.heads, h_step = me.heads * shares;
-    const E *q = p.q + t * p.q_token, *kk = p.k + t * p.k_token, *vv = p.v + t * p.v_token;
-    E *qo = p.q_out + t * p.qo_token;
     AppendSlot slot{-1, 0};
-    bool ready = false;
-    for (int u0 = 0; u0 < me.units; u0 += 32) {
-        const int u = me.unit + u0;
-        const bool on = u < me.units;
-        int ea, eb, pair;
-        RopeLane<W, HALF>::place(u, p.R, ea, eb, pair);
-        for (int h0 = h_first; h0 - me.head < H; h0 += kRopeUnits * h_step) {
-            Piece<E, W> a[kRopeUnits], b[kRopeUnits];
-#pragma unroll
-            for (int k = 0; k < kRopeUnits; ++k) {
-                const int h = h0 + k * h_step;
-                if (on && h < H) {
-                    const E *src = h < hq ? q + h * p.q_head : kk + (h - hq) * p.k_head;
-                    a[k] = *reinterpret_cast<const Piece<E, W> *>(src + ea);
-                    if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(src + eb);
-                }
-            }
-            if (!ready) {  // the first loads are in flight
-                slot = append_slot(p, t);
-                if (slot.cache < 0) return;
-                if (half > 0) rope_angles(cs, p.inv_freq, half, slot.pos, p.scale, false);
-                ready = true;
-            }
-            float2 c[W];
-            if (on && eb >= 0)
-#pragma unroll
-                for (int j = 0; j < W; ++j) c[j] = cs[pair + j];
-#pragma unroll
-            for (int k = 0; k < kRopeUnits; ++k) {
-                const int h = h0 + k * h_step;
-                if (on && h < H) {
-                    E *dst = h < hq ? qo + h * p.qo_head : p.k_cache + slot.cache + (h - hq) * p.c_head;
-                    if (eb >= 0) {
-                        rope_unit<E, W, HALF>(a[k], b[k], c);
-                        *reinterpret_cast<Piece<E, W> *>(dst + eb) = b[k];
-                    }
-                    *reinterpret_cast<Piece<E, W> *>(dst + ea) = a[k];
-                }
-            }
+    bool have = false;
+    auto ready = [&] {
+        if (!have) {
+            slot = append_slot(p, t);
+            if (slot.cache >= 0 && p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, slot.pos, p.scale, false);
+            have = true;
         }
+        return slot.cache >= 0;
+    };
+    int group = share;  // the warp's next group of heads; the key heads go on where the query heads end
+    if (p.q != nullptr) {
+        if (!rope_walk<E, W, HALF>(me, p.q + t * p.q_token, p.q_head, p.qo_head, p.Hq, p.R, group, shares, cs, true, ready,
+                                   [&] { return p.q_out + t * p.qo_token; }))
+            return;
+        group = (share + shares - (p.Hq + me.heads - 1) / me.heads % shares) % shares;
     }
-    if (!ready) {  // a share without a head
-        slot = append_slot(p, t);
-        if (slot.cache < 0) return;
-    }
+    if (!rope_walk<E, W, HALF>(me, p.k + t * p.k_token, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, true, ready,
+                               [&] { return p.k_cache + slot.cache; }))
+        return;
+    // The values: pieces of all heads in a row.
+    const E *vv = p.v + t * p.v_token;
     const int per_v = p.D / W, pieces = per_v * p.Hkv;
-    for (int i0 = share * 32 + lane; i0 - lane < pieces; i0 += kRopeUnits * 32 * shares) {
-        Piece<E, W> a[kRopeUnits];
+    for (int i0 = share * 32 + lane; i0 - lane < pieces; i0 += kRopeCopies * 32 * shares) {
+        Piece<E, W> a[kRopeCopies];
 #pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
+        for (int k = 0; k < kRopeCopies; ++k) {
             const int i = i0 + k * 32 * shares, h = i / per_v;
             if (i < pieces) a[k] = *reinterpret_cast<const Piece<E, W> *>(vv + h * p.v_head + (i - h * per_v) * W);
         }
+        if (!ready()) return;
 #pragma unroll
-        for (int k = 0; k < kRopeUnits; ++k) {
+        for (int k = 0; k < kRopeCopies; ++k) {
             const int i = i0 + k * 32 * shares, h = i / per_v;
             if (i < pieces)
                 *reinterpret_cast<Piece<E, W> *>(p.v_cache + slot.cache + h * p.c_head + (i - h * per_v) * W) = a[k];
