@@ -438,7 +438,7 @@ size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D,
  *   -inf logits are masked entries.  A row of only -inf has logsumexp -inf and NaN elsewhere; +inf or NaN
  *   in a row makes its values NaN.  NaN logits rank below all others.
  *   1 <= V <= 262144.  scale > 0, finite.  Rows of any alignment; 16-byte aligned rows are read faster.
- * Batch invariance: a row is cut into pieces of 16384 (bf16) or 8192 (fp32) elements, each reduced in one
+ * Batch invariance: a row is cut into pieces of 8192 (bf16) or 4096 (fp32) elements, each reduced in one
  * fixed order by one block and folded in one fixed tree.  How many blocks share a row's pieces depends on
  * M and changes no bit.
  */

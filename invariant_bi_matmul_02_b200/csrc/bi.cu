@@ -1189,9 +1189,9 @@ bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const 
     p.top_logprobs = top_logprobs;
     p.top_tokens = top_tokens;
     p.status = dev->status;
-    // Blocks that share a row: as many as keep all rows resident at once (two blocks an SM), none idle.
+    // Blocks that share a row: as many as keep all rows resident at once, none idle.
     p.cluster = bi::kTlMaxCluster;
-    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > 2 * (int64_t)dev->sms)) p.cluster /= 2;
+    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > (int64_t)bi::kTlBlocks * dev->sms)) p.cluster /= 2;
     const size_t smem = token_logprobs_smem((p.pieces + p.cluster - 1) / p.cluster, top_k);
     const bool vec = aligned16(x) && (M == 1 || ldx % (bf16 ? 8 : 4) == 0);
     void (*kernel)(bi::TlParams) = bf16 ? (vec ? bi::token_logprobs_kernel<true, true> : bi::token_logprobs_kernel<true, false>)

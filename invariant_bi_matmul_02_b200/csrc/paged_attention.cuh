@@ -83,13 +83,6 @@ __device__ __forceinline__ int pg_len(int L, int max_len)
     return L < 0 ? 0 : (L > max_len ? max_len : L);
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 8x8 b16 matrix in the mma register layout, transposed across the warp.
 __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
 {

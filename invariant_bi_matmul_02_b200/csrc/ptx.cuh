@@ -466,6 +466,14 @@ __device__ __forceinline__ void mma_16816_bf16(float (&d)[4], const uint32_t (&a
 
 namespace bi {
 
+// 2^x, to 2 units of the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Pairs of fp32 in one 64-bit register: sm_100a adds, multiplies and fuses two at a time, each rounded as
 // the single instruction rounds it.
 __device__ __forceinline__ uint64_t f2_pack(float a, float b)

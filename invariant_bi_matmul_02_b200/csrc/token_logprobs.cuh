@@ -8,8 +8,8 @@
 // Order (fixed by V and the type alone): the row is cut into pieces; in a piece each thread of the
 // block owns 64 consecutive bytes (32 bf16 or 16 fp32 elements, a group).  A warp takes the maximum of
 // its elements, then every thread's sums of e and e d over its group (two interleaved chains), then a
-// fixed butterfly: one (m, S, T) per (piece, warp).  These are folded at the end by one warp:
-// lane j folds triples j, j + 32, ... in order, then a fixed butterfly.  A row is taken by one block or
+// fixed butterfly: one (m, S, T) per (piece, warp).  These are folded at the end by one warp: against the
+// row's maximum, lane j adds triples j, j + 32, ... in order, then a fixed butterfly.  A row is taken by one block or
 // by a cluster of 2, 4 or 8 that share its pieces; the triples, and so the bits, are the same.
 //
 // The k best: only the groups' maxima are kept during the pass.
@@ -28,7 +28,8 @@
 
 namespace bi {
 
-constexpr int kTlThreads = 512;
+constexpr int kTlThreads = 256;
+constexpr int kTlBlocks = 4;                        // resident per SM, a bound on registers
 constexpr int kTlWarps = kTlThreads / 32;
 constexpr int kTlWords = 16;                        // 32-bit words per thread and piece
 constexpr int kTlMaxV = 262144;
@@ -36,7 +37,7 @@ constexpr int kTlMaxTop = 32;
 constexpr int kTlMaxCluster = 8;
 
 __host__ __device__ constexpr int tl_group(bool bf16) { return bf16 ? 2 * kTlWords : kTlWords; }
-__host__ __device__ constexpr int tl_piece(bool bf16) { return kTlThreads * tl_group(bf16); }  // 16384 or 8192
+__host__ __device__ constexpr int tl_piece(bool bf16) { return kTlThreads * tl_group(bf16); }  // 8192 or 4096
 constexpr int kTlMaxPieces = kTlMaxV / tl_piece(false);
 
 struct TlParams {
@@ -55,19 +56,6 @@ struct TlParams {
 struct TlTriple {
     float m, s, t;  // maximum of x, sum of e, sum of e * d in units of log2
 };
-
-// Symmetric in its arguments, so both lanes of a butterfly pair hold equal bits.
-__device__ __forceinline__ TlTriple tl_merge(TlTriple a, TlTriple b, float c)
-{
-    const float m = fmaxf(a.m, b.m), ref = m == kNegInf ? 0.0f : m;
-    // A side whose maximum is -inf has no terms: its offset is set to 0, its factor meets sums of 0.
-    const float da = a.m == kNegInf ? 0.0f : __fmul_rn(a.m - ref, c), db = b.m == kNegInf ? 0.0f : __fmul_rn(b.m - ref, c);
-    const float fa = exp2f(da), fb = exp2f(db);
-    // d grows by da: T' = f (T + s da).  With da = -inf (a range beyond fp32) f is 0 and the side is dropped.
-    const float ta = fa == 0.0f ? 0.0f : __fmul_rn(fa, __fadd_rn(a.t, __fmul_rn(a.s, da)));
-    const float tb = fb == 0.0f ? 0.0f : __fmul_rn(fb, __fadd_rn(b.t, __fmul_rn(b.s, db)));
-    return {m, __fadd_rn(__fmul_rn(fa, a.s), __fmul_rn(fb, b.s)), __fadd_rn(ta, tb)};
-}
 
 __device__ __forceinline__ float tl_logprob(float x, float m, float scale, float log_s)
 {
@@ -181,15 +169,49 @@ struct TlGroup {
     }
     __device__ __forceinline__ float max() const
     {
-        float m = kNegInf;
+        if (BF16) {
+            __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&w[0]);
 #pragma unroll
-        for (int i = 0; i < TlGroup<BF16>::kSize / 2; ++i) {
-            const float2 v = pair(i);
-            m = fmaxf(m, fmaxf(v.x, v.y));
+            for (int i = 1; i < kTlWords; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+            return fmaxf(__low2float(m), __high2float(m));
         }
+        float m = __uint_as_float(w[0]);
+#pragma unroll
+        for (int i = 1; i < kTlWords; ++i) m = fmaxf(m, __uint_as_float(w[i]));
         return m;
     }
+    // Sums of e = 2^((x - ref) c) and of e (x - ref) c over the group, in two interleaved chains.  A logit of
+    // -inf has e = 0 and would make 0 * -inf: CLAMP keeps the factor finite (below -1000 e is 0 already).
+    template <bool CLAMP>
+    __device__ __forceinline__ void sums(float ref, float c, float &s, float &t) const
+    {
+        const uint64_t neg = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
+        uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+        for (int i = 0; i < kSize / 2; ++i) {
+            const float2 v = pair(i);
+            uint64_t d2 = f2_mul(f2_add(f2_pack(v.x, v.y), neg), c2);
+            const float2 d = f2_unpack(d2);
+            const uint64_t e2 = f2_pack(ex2(d.x), ex2(d.y));
+            if (CLAMP) d2 = f2_pack(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f));
+            s2 = f2_add(s2, e2);
+            t2 = f2_fma(e2, d2, t2);
+        }
+        const float2 sv = f2_unpack(s2), tv = f2_unpack(t2);
+        s = __fadd_rn(sv.x, sv.y);
+        t = __fadd_rn(tv.x, tv.y);
+    }
 };
+
+// Sums of s and of t over the warp in a fixed tree, both at once: s in lanes 0 .. 15, t in lanes 16 .. 31.
+__device__ __forceinline__ float tl_warp_sums(float s, float t)
+{
+    const bool low = (threadIdx.x & 16) == 0;
+    float v = __fadd_rn(low ? s : t, __shfl_xor_sync(0xffffffffu, low ? t : s, 16));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
 
 template <bool BF16>
 __device__ __forceinline__ float tl_element(const void *row, int e)
@@ -204,57 +226,76 @@ constexpr int kTlKeys = 256;
 struct TlScratch {
     uint64_t keys[kTlKeys];
     int32_t groups[kTlGroups];
+    uint32_t range[2][kTlWarps];
     int32_t n_groups, n_keys;
 };
 
 // The block's `top` best keys, in order, to out[] (places without an element: 0).  tl_max holds its `local`
-// pieces' group maxima, one column per thread.
+// pieces' group maxima, one column per thread; `mine` is the ordered largest of
+// the thread's own (0: NaN or none).
 //   1. A bound that at least `top` groups reach: bisection over the ordered values of the threads' best
-//      groups, until no more than kTlGroups / 2 threads reach it (or it is exact).
+//      groups, until few more than `top` threads reach it (or it is exact).
 //   2. The groups that reach it are listed (more than one of a thread may), read again, and their elements
 //      that reach it listed: at least `top` elements do, so the best are among them.
 //   3. An element's place is the number of larger keys.
 // False when a list overflows: many equal values around the k-th.  All threads agree.
 template <bool BF16>
 __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *row, int rank, int local,
-                                               const float *tl_max, TlScratch &s, uint64_t *out)
+                                               const float *tl_max, uint32_t mine, TlScratch &s, uint64_t *out)
 {
     constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto first = [&](int i) { return (i * p.cluster + rank) * kPiece + kGroup * tid; };  // of the thread's i-th group
-    uint32_t mine = 0;
-    for (int i = 0; i < local; ++i) {
-        const uint32_t o = first(i) < p.V ? tl_order(tl_max[i * kTlThreads + tid]) : 0u;
-        mine = o > mine ? o : mine;
+    const uint32_t top_of_warp = __reduce_max_sync(0xffffffffu, mine), low_of_warp = __reduce_min_sync(0xffffffffu, mine);
+    if (lane == 0) {
+        s.range[0][warp] = low_of_warp;
+        s.range[1][warp] = top_of_warp;
     }
-    // Invariant: at least `top` threads reach lo, fewer reach hi.  With fewer than `top` groups lo stays 0.
     if (tid == 0) s.n_groups = s.n_keys = 0;
-    uint32_t lo = 0, hi = 0xffffffffu;
+    __syncthreads();
+    // Invariant: at least `top` threads reach lo (or lo is the least of all: every group is a candidate), fewer reach hi.
+    uint32_t lo = s.range[0][0], hi = s.range[1][0];
+#pragma unroll
+    for (int w = 1; w < kTlWarps; ++w) {
+        lo = min(lo, s.range[0][w]);
+        hi = max(hi, s.range[1][w]);
+    }
+    ++hi;
+    const int enough = 2 * p.top + 8;
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         const int n = __syncthreads_count(mine >= mid);
         if (n >= p.top) lo = mid;
         else hi = mid;
-        if (n >= p.top && n <= kTlGroups / 2) break;
+        if (n >= p.top && n <= enough) break;
     }
-    __syncthreads();
-    for (int i = 0; i < local; ++i)
-        if (first(i) < p.V && tl_order(tl_max[i * kTlThreads + tid]) >= lo) {
-            const int at = atomicAdd(&s.n_groups, 1);
-            if (at < kTlGroups) s.groups[at] = first(i);
-        }
+    if (mine >= lo) {
+#pragma unroll 4
+        for (int i = 0; i < local; ++i)
+            if (tl_order(tl_max[i * kTlThreads + tid]) >= lo && first(i) < p.V) {
+                const int at = atomicAdd(&s.n_groups, 1);
+                if (at < kTlGroups) s.groups[at] = first(i);
+            }
+    }
     __syncthreads();
     const int n_groups = s.n_groups;
     if (n_groups > kTlGroups) return false;
-    for (int g = warp; g < n_groups; g += kTlWarps) {
-        const int e = s.groups[g] + lane;
-        if (lane < kGroup && e < p.V) {
-            const float v = tl_element<BF16>(row, e);
-            if (tl_order(v) >= lo) {
-                const int at = atomicAdd(&s.n_keys, 1);
-                if (at < kTlKeys) s.keys[at] = tl_key(v, (uint32_t)e);
-            }
+    constexpr int kBatch = 4;  // elements a thread has in flight
+    for (int i0 = tid; i0 - tid < n_groups * kGroup; i0 += kBatch * kTlThreads) {
+        float v[kBatch];
+        int e[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kTlThreads;
+            e[k] = i < n_groups * kGroup ? s.groups[i / kGroup] + i % kGroup : p.V;
+            v[k] = e[k] < p.V ? tl_element<BF16>(row, e[k]) : 0.0f;
         }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (e[k] < p.V && tl_order(v[k]) >= lo) {
+                const int at = atomicAdd(&s.n_keys, 1);
+                if (at < kTlKeys) s.keys[at] = tl_key(v[k], (uint32_t)e[k]);
+            }
     }
     if (tid < kTlMaxTop) out[tid] = 0;
     __syncthreads();
@@ -272,7 +313,7 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
 // Grid M * cluster blocks of kTlThreads; block r of a row's cluster takes pieces r, r + cluster, ...
 // Dynamic shared memory: the block's group maxima, kTlThreads floats per piece (top > 0 only).
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlParams p)
+__global__ void __launch_bounds__(kTlThreads, kTlBlocks) token_logprobs_kernel(const TlParams p)
 {
     namespace cg = cooperative_groups;
     constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
@@ -295,43 +336,50 @@ __global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlP
     griddep_wait();
     griddep_launch_dependents();
 
-    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    // The scored logit is on its way while the row is read.
+    int32_t tok = -1;
+    float tok_x = 0.0f;
+    if (rank == 0 && tid == 0 && p.logprobs != nullptr) {
+        tok = p.tokens[r];
+        if (tok >= 0 && tok < p.V) tok_x = tl_element<BF16>(row, tok);
+    }
     TlGroup<BF16> g, next;
     int local = 0;
+    bool masked = false;
+    float thread_best = __int_as_float(0x7fffffff);  // NaN: none yet
     if (rank < p.pieces) g.template load<VEC>(row, rank * kPiece + kGroup * tid, p.V);
     for (int piece = rank; piece < p.pieces; piece += p.cluster, ++local) {
         const int ahead = piece + p.cluster;
         if (ahead < p.pieces) next.template load<VEC>(row, ahead * kPiece + kGroup * tid, p.V);
         const float gm = g.max();
-        if (p.top > 0) tl_max[local * kTlThreads + tid] = gm;
+        if (p.top > 0) {
+            tl_max[local * kTlThreads + tid] = gm;
+            if (piece * kPiece + kGroup * tid < p.V) thread_best = fmaxf(thread_best, gm);
+        }
         float m = gm;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float ref = m == kNegInf ? 0.0f : m;
-        const uint64_t neg = f2_pack(-ref, -ref);
-        uint64_t s2 = 0, t2 = 0;
-#pragma unroll
-        for (int i = 0; i < TlGroup<BF16>::kSize / 2; ++i) {
-            const float2 v = g.pair(i);
-            const uint64_t d2 = f2_mul(f2_add(f2_pack(v.x, v.y), neg), c2);
-            const float2 d = f2_unpack(d2);
-            float ex, ey;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(d.x));
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(d.y));
-            const uint64_t e2 = f2_pack(ex, ey);
-            s2 = f2_add(s2, e2);
-            // -inf would make 0 * -inf: below -1000 the factor is 0 already.
-            t2 = f2_fma(e2, f2_pack(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f)), t2);
+        float s, t;
+        if (!masked) {
+            g.template sums<false>(ref, p.scale_log2, s, t);
+            masked = __any_sync(0xffffffffu, t != t);  // a mask of -inf (or a NaN): once more, and from now on
         }
-        const float2 sv = f2_unpack(s2), tv = f2_unpack(t2);
-        const float s = warp_sum(__fadd_rn(sv.x, sv.y)), t = warp_sum(__fadd_rn(tv.x, tv.y));
-        if (lane == 0) triples[piece * kTlWarps + warp] = TlTriple{m, s, t};
+        if (masked) g.template sums<true>(ref, p.scale_log2, s, t);
+        const float v = tl_warp_sums(s, t);
+        TlTriple &to = triples[piece * kTlWarps + warp];
+        if (lane == 0) {
+            to.m = m;
+            to.s = v;
+        } else if (lane == 16) {
+            to.t = v;
+        }
         g = next;
     }
     __syncthreads();
 
     if (p.top > 0) {
-        const bool found = tl_best_groups<BF16>(p, row, rank, local, tl_max, scratch, bests[rank]);
+        const bool found = tl_best_groups<BF16>(p, row, rank, local, tl_max, tl_order(thread_best), scratch, bests[rank]);
         if (!found && warp == 0) {
             // Too many groups or elements tie near the k-th: warp 0 walks the maxima in index order and reads
             // again only the groups that beat the k-th key so far.
@@ -359,55 +407,72 @@ __global__ void __launch_bounds__(kTlThreads, 2) token_logprobs_kernel(const TlP
         __syncthreads();
     }
 
-    // Warp 0 folds the triples; the block's upper half places the blocks' keys among one another.
-    uint64_t key = 0;
-    int place = 0;
-    if (warp == 0) {
-        TlTriple a{kNegInf, 0.0f, 0.0f};
-        for (int i = lane; i < p.pieces * kTlWarps; i += 32) a = tl_merge(a, triple[i], p.scale_log2);
+    // A key's place is the number of larger ones: its own list is in order (unused places hold 0), in every other
+    // list it is searched for.
+    constexpr int kLists = (kTlMaxCluster + kTlWarps - 1) / kTlWarps;  // of a warp
+    uint64_t key[kLists];
+    int place[kLists];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const TlTriple b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                             __shfl_xor_sync(0xffffffffu, a.t, o)};
-            a = tl_merge(a, b, p.scale_log2);
+    for (int i = 0; i < kLists; ++i) {
+        const int q = warp + i * kTlWarps;
+        key[i] = q < p.cluster && lane < p.top ? best[q][lane] : 0;
+        place[i] = lane;
+        if (key[i] != 0)
+#pragma unroll
+            for (int o = 0; o < kTlMaxCluster; ++o)
+                if (o < p.cluster && o != q) {
+                    int n = 0;
+#pragma unroll
+                    for (int step = 16; step > 0; step >>= 1) n += best[o][n + step - 1] > key[i] ? step : 0;
+                    place[i] += n + (best[o][n] > key[i]);
+                }
+    }
+    if (warp == 0) {
+        // Fold the triples: the maximum is exact in any order; lane j adds triples j, j + 32, ... in order.
+        const int n = p.pieces * kTlWarps;
+        float m = kNegInf;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, triple[i].m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m == kNegInf ? 0.0f : m;
+        float s = 0.0f, t = 0.0f;
+        for (int i = lane; i < n; i += 32) {
+            const TlTriple v = triple[i];
+            // Against the row's maximum the triple's d all grow by d: S' = f S, T' = f (T + S d).  A triple without
+            // finite elements has S = T = 0; where f is 0 its terms are.
+            const float d = v.m == kNegInf ? 0.0f : __fmul_rn(v.m - ref, p.scale_log2), f = exp2f(d);
+            s = __fadd_rn(s, __fmul_rn(f, v.s));
+            t = __fadd_rn(t, f == 0.0f ? 0.0f : __fmul_rn(f, __fadd_rn(v.t, __fmul_rn(v.s, d))));
         }
+        const float sums = tl_warp_sums(s, t);
+        TlTriple a{m, __shfl_sync(0xffffffffu, sums, 0), __shfl_sync(0xffffffffu, sums, 16)};
         // A row without a finite maximum has no distribution: all its values are NaN.
         const float log_s = logf(a.s);
         if (lane == 0) {
             row_m = a.m;
             row_log_s = log_s;
             if (p.logprobs != nullptr) {
-                const int32_t tok = p.tokens[r];
                 float v = 0.0f;  // a negative token: the row is not scored
                 if (tok >= p.V) {
                     *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
                     v = __int_as_float(0x7fffffff);
                 } else if (tok >= 0) {
-                    v = tl_logprob(tl_element<BF16>(row, tok), a.m, p.scale, log_s);
+                    v = tl_logprob(tok_x, a.m, p.scale, log_s);
                 }
                 p.logprobs[r] = v;
             }
             if (p.entropy != nullptr) p.entropy[r] = __fsub_rn(log_s, __fmul_rn(0.693147180559945309f, a.t / a.s));
             if (p.logsumexp != nullptr) p.logsumexp[r] = __fmaf_rn(a.m, p.scale, log_s);
         }
-    } else if (tid >= kTlThreads / 2 && p.top > 0) {
-        // A key's place is the number of larger ones: its own list is in order (unused places hold 0).
-        const int q = (tid - kTlThreads / 2) >> 5;
-        place = lane;
-        if (q < p.cluster && lane < p.top) {
-            key = best[q][lane];
-            for (int o = 0; o < p.cluster; ++o)
-                if (o != q)
-#pragma unroll 4
-                    for (int j = 0; j < p.top; ++j) place += best[o][j] > key;
-        }
     }
     if (p.top == 0) return;
     __syncthreads();
-    if (key != 0 && place < p.top) {
-        p.top_logprobs[r * p.top + place] = tl_logprob(tl_value((uint32_t)(key >> 32)), row_m, p.scale, row_log_s);
-        p.top_tokens[r * p.top + place] = (int32_t)~(uint32_t)key;
-    }
+#pragma unroll
+    for (int i = 0; i < kLists; ++i)
+        if (key[i] != 0 && place[i] < p.top) {
+            p.top_logprobs[r * p.top + place[i]] = tl_logprob(tl_value((uint32_t)(key[i] >> 32)), row_m, p.scale, row_log_s);
+            p.top_tokens[r * p.top + place[i]] = (int32_t)~(uint32_t)key[i];
+        }
 }
 
 }  // namespace bi
