@@ -466,6 +466,14 @@ __device__ __forceinline__ void mma_16816_bf16(float (&d)[4], const uint32_t (&a
 
 namespace bi {
 
+// 32 bytes (aligned) that are read once: past the L1, first to leave the L2.
+__device__ __forceinline__ void load_32(const void *p, uint32_t *w)
+{
+    asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
 // 2^x, to 2 units of the last place; results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x)
 {

@@ -115,8 +115,15 @@ struct TlGroup {
         constexpr int kBytes = BF16 ? 2 : 4, kPer16 = 16 / kBytes;
         const uint8_t *at = static_cast<const uint8_t *>(row) + (int64_t)e0 * kBytes;
         if (VEC && e0 + kSize <= V) {
+            // A lane's pieces are 64 bytes from the next lane's: 32-byte loads take each sector once, 16-byte
+            // ones leave its other half to the L1.
+            if ((reinterpret_cast<uintptr_t>(at) & 31u) == 0) {
 #pragma unroll
-            for (int i = 0; i < kTlWords / 4; ++i) put(i, __ldcs(reinterpret_cast<const uint4 *>(at) + i));
+                for (int i = 0; i < kTlWords / 8; ++i) load_32(at + 32 * i, w + 8 * i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTlWords / 4; ++i) put(i, __ldcs(reinterpret_cast<const uint4 *>(at) + i));
+            }
             return;
         }
         if (!VEC && e0 > 0 && e0 + kSize + kPer16 <= V) {
