@@ -227,14 +227,16 @@ __device__ __forceinline__ float tl_element(const void *row, int e)
     return static_cast<const float *>(row)[e];
 }
 
-constexpr int kTlGroups = 128;  // candidate groups and elements the short way takes
+constexpr int kTlColumns = 128;  // candidate threads, groups and elements the short way takes
+constexpr int kTlGroups = 128;
 constexpr int kTlKeys = 256;
 
 struct TlScratch {
     uint64_t keys[kTlKeys];
     int32_t groups[kTlGroups];
     uint32_t range[2][kTlWarps];
-    int32_t n_groups, n_keys;
+    int32_t columns[kTlColumns];
+    int32_t n_columns, n_groups, n_keys;
 };
 
 // The block's `top` best keys, in order, to out[] (places without an element: 0).  tl_max holds its `local`
@@ -242,7 +244,7 @@ struct TlScratch {
 // the thread's own (0: NaN or none).
 //   1. A bound that at least `top` groups reach: bisection over the ordered values of the threads' best
 //      groups, until few more than `top` threads reach it (or it is exact).
-//   2. The groups that reach it are listed (more than one of a thread may), read again, and their elements
+//   2. The groups of those threads that reach it are listed, read again, and their elements
 //      that reach it listed: at least `top` elements do, so the best are among them.
 //   3. An element's place is the number of larger keys.
 // False when a list overflows: many equal values around the k-th.  All threads agree.
@@ -252,13 +254,12 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
 {
     constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto first = [&](int i) { return (i * p.cluster + rank) * kPiece + kGroup * tid; };  // of the thread's i-th group
     const uint32_t top_of_warp = __reduce_max_sync(0xffffffffu, mine), low_of_warp = __reduce_min_sync(0xffffffffu, mine);
     if (lane == 0) {
         s.range[0][warp] = low_of_warp;
         s.range[1][warp] = top_of_warp;
     }
-    if (tid == 0) s.n_groups = s.n_keys = 0;
+    if (tid == 0) s.n_columns = s.n_groups = s.n_keys = 0;
     __syncthreads();
     // Invariant: at least `top` threads reach lo (or lo is the least of all: every group is a candidate), fewer reach hi.
     uint32_t lo = s.range[0][0], hi = s.range[1][0];
@@ -277,12 +278,19 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
         if (n >= p.top && n <= enough) break;
     }
     if (mine >= lo) {
-#pragma unroll 4
-        for (int i = 0; i < local; ++i)
-            if (tl_order(tl_max[i * kTlThreads + tid]) >= lo && first(i) < p.V) {
-                const int at = atomicAdd(&s.n_groups, 1);
-                if (at < kTlGroups) s.groups[at] = first(i);
-            }
+        const int at = atomicAdd(&s.n_columns, 1);
+        if (at < kTlColumns) s.columns[at] = tid;
+    }
+    __syncthreads();
+    const int n_columns = s.n_columns;
+    if (n_columns > kTlColumns) return false;
+    for (int j = tid; j < n_columns * local; j += kTlThreads) {
+        const int column = s.columns[j / local], piece = j % local;
+        const int e0 = (piece * p.cluster + rank) * kPiece + kGroup * column;
+        if (tl_order(tl_max[piece * kTlThreads + column]) >= lo && e0 < p.V) {
+            const int at = atomicAdd(&s.n_groups, 1);
+            if (at < kTlGroups) s.groups[at] = e0;
+        }
     }
     __syncthreads();
     const int n_groups = s.n_groups;
