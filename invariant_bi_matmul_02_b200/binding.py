@@ -3,7 +3,9 @@
 Argument marshalling only.  Each function checks device, dtype and layout of the
 torch tensors it is given, allocates the output with torch when none is passed,
 and calls the C entry point of the same name with raw device pointers, leading
-dimensions and the current CUDA stream.  Every step of the computation runs in
+dimensions and the current CUDA stream.  The operators of a decode step (rotation, paged
+cache, token log-probabilities) do this in the extension module _marshal, whose calls
+cost a fraction of the Python checks.  Every step of the computation runs in
 libbi.so's kernels; there is no fallback.  If libbi.so is missing or a call fails
 the function raises.
 """
@@ -21,7 +23,6 @@ LIB_PATH = os.path.join(_HERE, "libbi.so")
 BI_OK, BI_ERR_INVALID_ARG, BI_ERR_UNSUPPORTED, BI_ERR_ALIGNMENT, BI_ERR_CUDA, BI_ERR_TIMEOUT = range(6)
 BI_BF16, BI_F32 = 0, 1
 BI_B_KN, BI_B_NK = 0, 1
-BI_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 # Kinds of bi_rope_freqs and the parameters each takes, in order.
 BI_ROPE_KINDS = {"plain": (0, ()), "linear": (1, ("factor",)), "ntk": (2, ("factor",)),
                  "yarn": (3, ("factor", "original_length", "beta_fast", "beta_slow")),
@@ -414,29 +415,25 @@ def bi_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     return out
 
 
-def _heads(t: torch.Tensor, name: str, dtypes, cur: int | None) -> int:
-    """Check a [T, H, D] tensor whose heads' entries are consecutive; returns the current device."""
-    cur = _need_cuda(t, name, dtypes, cur)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, H, D]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}: a head's entries must be contiguous")
-    return cur
+_marshal = None
 
 
-def _vector(t: torch.Tensor, name: str, dtype, n: int | None, cur: int) -> int:
-    """Check a contiguous vector (of n entries, if n is given); returns its address."""
-    _need_cuda(t, name, (dtype,), cur)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a vector" + ("" if n is None else f" of {n}"))
-    _contig(t, name)
-    return t.data_ptr()
-
-
-def _rope_layout(layout: str) -> int:
-    if layout not in BI_ROPE_LAYOUTS:
-        raise ValueError("layout must be 'half' (pairs i, i + R/2) or 'interleaved' (pairs 2i, 2i + 1)")
-    return BI_ROPE_LAYOUTS[layout]
+def load_marshal():
+    """The extension module that checks and passes the arguments of the operators below (once), bound to
+    the loaded library's entry points."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("the binding's extension module _marshal.so is missing or does not load: build it with "
+                               "__graft_entry__.build() or invariant_bi_matmul_02_b200/csrc/build.py") from e
+        m.bind(BiError, *[ctypes.cast(getattr(lib, n), _p).value for n in (
+            "bi_rope", "bi_paged_append", "bi_paged_decode_attention", "bi_paged_decode_attention_scratch_bytes",
+            "bi_token_logprobs")])
+        _marshal = m
+    return _marshal
 
 
 def bi_rope_freqs(rotary_dim: int, theta: float = 10000.0, kind: str = "plain", device=None,
@@ -466,42 +463,8 @@ def bi_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
             scale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x [T, H, D] (bf16 or fp32, token and head strides free) with the first 2 * len(inv_freq) entries of
     every head turned by positions [T] (int32); `inverse` turns back (the gradient's map).  out may be x."""
-    cur = _heads(x, "x", (torch.bfloat16, torch.float32), None)
-    T, H, D = x.shape
-    pos = _vector(positions, "positions", torch.int32, T, cur)
-    freq = _vector(inv_freq, "inv_freq", torch.float64, None, cur)
-    if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    _heads(out, "out", (x.dtype,), cur)
-    if tuple(out.shape) != (T, H, D):
-        raise ValueError("out must be [T, H, D]")
-    _check("bi_rope", load().bi_rope(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-                                     out.stride(1), _DT[x.dtype], pos, freq, T, H, D, 2 * inv_freq.shape[0],
-                                     _rope_layout(layout), float(scale), 1 if inverse else 0, _stream(stream, cur)))
-    return out
-
-
-def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, cur: int) -> PagedCache:
-    """The cache description of two [pages, page_size, heads, D] tensors with the same strides."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need_cuda(t, n, (torch.bfloat16,), cur)
-        if t.dim() != 4:
-            raise ValueError(f"{n} must be [pages, page_size, heads, D] (a transposed view for pages laid out head first)")
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"{n}: a head's entries must be contiguous")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    pages, page_size, heads, dim = k_cache.shape
-    s = k_cache.stride()
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, heads, dim, s[0], s[1], s[2])
-
-
-def _block_table(t: torch.Tensor, B: int, cur: int):
-    """Check a [B, max_pages] int32 table with contiguous rows: its address, row stride and width."""
-    _need_cuda(t, "block_table", (torch.int32,), cur)
-    if t.dim() != 2 or t.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    return t.data_ptr(), _ld(t, "block_table"), t.shape[1]
+    return (_marshal or load_marshal()).rope(x, positions, inv_freq, layout, scale, inverse, out,
+                                             stream if stream is None else _stream(stream))
 
 
 def bi_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -514,43 +477,9 @@ def bi_paged_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     new tokens, which come last; cu_new [B+1] delimits them (None: one per sequence); positions [T] replaces
     the places that turn them.  q_out may be q.  Tokens that are skipped (behind cu_new[B], or of a sequence of
     length 0) leave their q_out rows as they were."""
-    bf16 = (torch.bfloat16,)
-    cur = _heads(k, "k", bf16, None)
-    _heads(v, "v", bf16, cur)
-    cache = _paged_cache(k_cache, v_cache, cur)
-    T = k.shape[0]
-    if tuple(k.shape) != (T, cache.heads, cache.head_dim) or v.shape != k.shape:
-        raise ValueError("k and v must be [T, heads, D] of the cache's heads and D")
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    lens = _vector(seq_lens, "seq_lens", torch.int32, None, cur)
-    table, table_stride, max_pages = _block_table(block_table, B, cur)
-    if cu_new is None and T != B:
-        raise ValueError("without cu_new every sequence has one new token: k must have B tokens")
-    cu = None if cu_new is None else _vector(cu_new, "cu_new", torch.int32, B + 1, cur)
-    pos = None if positions is None else _vector(positions, "positions", torch.int32, T, cur)
-    freq, R = None, 0
-    if inv_freq is not None:
-        freq, R = _vector(inv_freq, "inv_freq", torch.float64, None, cur), 2 * inv_freq.shape[0]
-    qs, os, Hq = (None, 0, 0), (None, 0, 0), 0
-    if q is not None:
-        _heads(q, "q", bf16, cur)
-        Hq = q.shape[1]
-        if tuple(q.shape) != (T, Hq, cache.head_dim):
-            raise ValueError("q must be [T, Hq, D]")
-        if q_out is None:
-            q_out = torch.empty((T, Hq, cache.head_dim), dtype=q.dtype, device=q.device)
-        _heads(q_out, "q_out", bf16, cur)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must be [T, Hq, D]")
-        if Hq > 0:
-            qs, os = (q.data_ptr(), q.stride(0), q.stride(1)), (q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _check("bi_paged_append", load().bi_paged_append(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), *qs, *os, Hq,
-        ctypes.byref(cache), table, table_stride, max_pages, lens, cu, pos, freq, R, _rope_layout(layout),
-        float(scale), T, B, _stream(stream, cur)))
-    return q_out
+    return (_marshal or load_marshal()).paged_append(
+        k, v, k_cache, v_cache, block_table, seq_lens, cu_new, inv_freq, layout, scale, q, q_out, positions,
+        stream if stream is None else _stream(stream))
 
 
 def bi_paged_decode_attention_scratch_bytes(B: int, Hq: int, D: int, max_len: int) -> int:
@@ -563,38 +492,11 @@ def bi_paged_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
                               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One decode step over a paged cache: q [B, Hq, D] (rows may be strided), caches [pages, page_size, heads, D],
     block_table [B, max_pages] and seq_lens [B] int32.  max_len: the longest sequence as the host knows it (default:
-    all the table can name; a tighter bound needs less scratch)."""
-    cur = _heads(q, "q", (torch.bfloat16,), None)
-    cache = _paged_cache(k_cache, v_cache, cur)
-    B, Hq, D = q.shape
-    if D != cache.head_dim:
-        raise ValueError("q's head size differs from the cache's")
-    if Hq > 1 and q.stride(1) != D:
-        raise ValueError("q: a token's heads must be contiguous")
-    lens = _vector(seq_lens, "seq_lens", torch.int32, B, cur)
-    table, table_stride, max_pages = _block_table(block_table, B, cur)
-    if max_len is None:
-        max_len = max_pages * cache.page_size
-    if scale is None:
-        scale = D ** -0.5
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-    _need_cuda(out, "out", (torch.bfloat16,), cur)
-    _contig(out, "out")
-    if tuple(out.shape) != (B, Hq, D):
-        raise ValueError("out must be [B, Hq, D]")
-    if scratch is None:
-        scratch = torch.empty(max(bi_paged_decode_attention_scratch_bytes(B, Hq, D, max_len), 16), dtype=torch.uint8,
-                              device=q.device)
-    if not scratch.is_cuda:
-        raise ValueError("scratch must be device memory")
-    _same_device(scratch.get_device(), "scratch", cur)
-    _contig(scratch, "scratch")
-    nbytes = scratch.numel() * scratch.element_size()
-    _check("bi_paged_decode_attention", load().bi_paged_decode_attention(
-        q.data_ptr(), q.stride(0), ctypes.byref(cache), table, table_stride, max_pages, lens, out.data_ptr(), B, Hq,
-        int(max_len), float(scale), scratch.data_ptr(), nbytes, _stream(stream, cur)))
-    return out
+    all the table can name; a tighter bound needs less scratch).  scratch: device memory of at least
+    bi_paged_decode_attention_scratch_bytes, allocated when None (not on a stream other than the current one)."""
+    return (_marshal or load_marshal()).paged_decode_attention(
+        q, k_cache, v_cache, block_table, seq_lens, max_len, scale, scratch, out,
+        stream if stream is None else _stream(stream))
 
 
 class TokenLogprobs(NamedTuple):
@@ -611,21 +513,8 @@ def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     """Per row of logits [M, V] (fp32 or bf16, rows may be strided) times `scale` (1 / temperature): the
     log-probability of tokens [M] (int32; negative: not scored, 0), the entropy, the logsumexp and the top_k best
     log-probabilities with their tokens."""
-    cur = _need_cuda(logits, "logits", (torch.float32, torch.bfloat16))
-    ld = _ld(logits, "logits")
-    M, V = logits.shape
-    top_k = int(top_k)
-    if not 0 <= top_k <= V:
-        raise ValueError("top_k must be in 0 .. V")
-    tok = None if tokens is None else _vector(tokens, "tokens", torch.int32, M, cur)
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    r = TokenLogprobs(None if tokens is None else torch.empty(M, **f32), torch.empty(M, **f32), torch.empty(M, **f32),
-                      torch.empty((M, top_k), **f32), torch.empty((M, top_k), dtype=torch.int32, device=logits.device))
-    _check("bi_token_logprobs", load().bi_token_logprobs(
-        logits.data_ptr(), ld, _DT[logits.dtype], tok, float(scale), top_k,
-        None if tokens is None else r.logprobs.data_ptr(), r.entropy.data_ptr(), r.logsumexp.data_ptr(),
-        r.top_logprobs.data_ptr(), r.top_tokens.data_ptr(), M, V, _stream(stream, cur)))
-    return r
+    return TokenLogprobs._make((_marshal or load_marshal()).token_logprobs(
+        logits, tokens, top_k, scale, stream if stream is None else _stream(stream)))
 
 
 def bi_get_device_status(stream=None) -> int:

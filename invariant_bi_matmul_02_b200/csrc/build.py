@@ -43,6 +43,29 @@ def build(force: bool = False, out: str = LIB, defines=(), verbose: bool = False
     return out
 
 
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+
+
+def build_marshal(force: bool = False) -> str:
+    """The binding's extension module (argument marshalling only; no kernels), against torch's headers."""
+    deps = [MARSHAL_SRC, os.path.join(INCLUDE, "bi.h")]
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= max(os.path.getmtime(p) for p in deps):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-o", MARSHAL, MARSHAL_SRC,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    return MARSHAL
+
+
 PROBE_SRC = os.path.join(CSRC, "mma_probe.cu")
 PROBE = os.path.join(PKG, "mma_probe")
 
@@ -60,3 +83,4 @@ def build_probe(force: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_marshal(force="--force" in sys.argv))
