@@ -394,9 +394,9 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
  * over the sequence's t < seq_lens[b].  A sequence of length 0 (an empty place of a padded batch) gets zeros.
  * Passage: as bi_decode_attention.
  *
- * Batch invariance: a sequence is cut into splits of 256 tokens and tiles of 32, cuts fixed by the token's
- * own place; scores are fp32 dot products, four chains take the split's tiles w and w + 4 under a running
- * maximum and are folded in order, and splits in a tree fixed by their number.  A sequence's output does not depend on
+ * Batch invariance: a sequence is one split up to 512 tokens and splits of 256 beyond, in tiles of 32, cuts
+ * fixed by its own length; scores are fp32 dot products, four chains take a split's tiles w, w + 4, ... under
+ * a running maximum and are folded in order, and splits in a tree fixed by their number.  A sequence's output does not depend on
  * the others, on where its pages lie, on the page size or on max_len.
  *
  *   q        device, bf16, [B, Hq, D], heads consecutive, sequences q_stride elements apart (a multiple of 8).
@@ -410,7 +410,7 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
  *   than 8 tokens, or of an odd number, take more and smaller copies); B, Hq <= 65535 and
  *   min(B, 2048) * heads * ceil(max_len / 256) < 2^31.
  *   scratch  caller-owned device memory, 16-byte aligned, bi_paged_decode_attention_scratch_bytes bytes;
- *            overwritten (two launches on `stream` per 2048 sequences; one when max_len <= 256), so
+ *            overwritten (two launches on `stream` per 2048 sequences; one when max_len <= 512), so
  *            overlapping calls need separate scratch.
  *   q, out 16-byte aligned.
  */
@@ -419,7 +419,7 @@ bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_pa
                                     const int32_t *seq_lens, void *out, int64_t B, int64_t Hq, int64_t max_len,
                                     float scale, void *scratch, size_t scratch_bytes, void *stream);
 
-/* Bytes of scratch bi_paged_decode_attention needs (0 if any size is <= 0 or max_len <= 256). */
+/* Bytes of scratch bi_paged_decode_attention needs (0 if any size is <= 0 or max_len <= 512). */
 size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len);
 
 /*

@@ -582,9 +582,14 @@ bi_status launch_paged(dim3 grid, cudaStream_t s, const CUtensorMap &tm_k, const
     const bi_status st = launch_pdl(bi::paged_attention_split_kernel<D, NT>, grid, dim3(bi::kPgThreads),
                                     (size_t)bi::PgShape<D>::kSmem, s, tm_k, tm_v, p);
     if (st != BI_OK || p.S == 1) return st;  // one split per sequence: launch 1 wrote out
-    return launch_pdl(bi::paged_attention_combine_kernel<D>, dim3((unsigned)p.Hq, (unsigned)p.B),
-                      dim3(bi::kPgCombineThreads), 0, s, static_cast<const float2 *>(p.part_ml),
-                      static_cast<const float *>(p.part_o), p.lens, p.out, (int)p.Hq, (int)p.S, (int)p.max_len);
+    const float2 *ml = p.part_ml;
+    const float *o = p.part_o;
+    if (p.S > bi::kPgSerial)
+        return launch_pdl(bi::paged_attention_combine_long_kernel<D>, dim3(D / 32, (unsigned)p.Hq, (unsigned)p.B),
+                          dim3(bi::kPgCombineThreads), 0, s, ml, o, p.lens, p.out, (int)p.Hq, (int)p.S, (int)p.max_len);
+    const int rows = p.B * p.Hq, per_block = bi::kPgCombineThreads / (D / 4);
+    return launch_pdl(bi::paged_attention_combine_kernel<D>, dim3((unsigned)((rows + per_block - 1) / per_block)),
+                      dim3(bi::kPgCombineThreads), 0, s, ml, o, p.lens, p.out, (int)p.Hq, (int)p.S, (int)p.max_len, rows);
 }
 
 inline unsigned elementwise_blocks(int64_t work, int sms)
@@ -1074,7 +1079,7 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
 
 size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len)
 {
-    if (B <= 0 || Hq <= 0 || D <= 0 || max_len <= bi::kPgSplit) return 0;
+    if (B <= 0 || Hq <= 0 || D <= 0 || bi::pg_splits(max_len) <= 1) return 0;
     const size_t parts = (size_t)(B < bi::kPgSeqs ? B : bi::kPgSeqs) * (size_t)Hq * (size_t)bi::pg_splits(max_len);
     return parts * ((size_t)D * sizeof(float) + sizeof(float2));
 }

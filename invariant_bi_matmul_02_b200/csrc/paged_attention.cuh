@@ -2,9 +2,10 @@
 // sequence).
 //
 // The cache is pages of P tokens; a sequence's block table names its pages in order.  Sequence b's
-// L_b tokens are cut into splits of kPgSplit tokens and each split into tiles of kPgTile tokens, cuts
-// fixed by the token's own place.  A (split, kv head) is taken by a group of four warps: warp w takes tiles w and
-// w + 4, with a running maximum; scores, weights and the weighted value sum never leave the warp.  The
+// L_b tokens are one split up to kPgWhole tokens (no second launch: 300 tokens of one sequence take 5.9 us, and 7.5
+// as two splits of 256), otherwise splits of kPgSplit tokens, and each split is cut into tiles of kPgTile
+// tokens: cuts fixed by the sequence's own length.  A (split, kv head) is taken by a group of four warps: warp
+// w takes tiles w, w + 4, ..., with a running maximum; scores, weights and the weighted value sum never leave the warp.  The
 // four warps are then folded in order through shared memory; a sequence of one split is
 // written out at once, the splits of a longer one go to scratch and are folded by the second launch
 // in a tree fixed by the number of splits.  So a sequence's output depends on its own query, tokens
@@ -13,10 +14,11 @@
 // Bound by the cache's bytes.  One persistent CTA per SM; the (split, kv head) items of the batch are
 // numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
 // how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
-// other's arithmetic and loads.  The producer warp fills a ring of tiles (K and V of 32 tokens: 16 KB at
+// other's arithmetic and loads.  The producers fill a ring of tiles (K and V of 32 tokens: 16 KB at
 // head size 128, 12 tiles; 8 KB at 64, 24 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
-// entries, each within one page and completing on the tile's mbarrier.  The lanes look the item's
-// pages up one item ahead and each issues the boxes of its own pages.
+// entries, each within one page and completing on the tile's mbarrier.  The lanes look pages up one chunk of
+// 32 boxes ahead and each issues its own box.  Four producer warps issue alternate tiles: one warp needs about
+// 1000 cycles a tile in pages of 16 (wait, barrier, 8 copies), more than a tile takes to arrive.
 //
 // Tensor-core work (mma.sync m16n8k16, bf16 in, fp32 accumulate): S^T = K Q^T with tokens on the 16
 // rows and the group's heads on the 8 columns (two column tiles for groups of 9 to 16), then
@@ -40,6 +42,7 @@ constexpr int kPgWarps = 8;                      // consumer warps
 constexpr int kPgGroups = 2;                     // consumer groups, alternate items
 constexpr int kPgGroupWarps = kPgWarps / kPgGroups;
 constexpr int kPgSplit = 256;                    // tokens per split: two tiles for each warp of a group
+constexpr int kPgWhole = 512;                    // a sequence of up to this many tokens is one split
 constexpr int kPgProducers = 4;                  // producer warps
 constexpr int kPgThreads = 32 * (kPgWarps + kPgProducers);
 constexpr int kPgFold = 4;                       // query heads folded at a time
@@ -75,7 +78,10 @@ struct PgParams {
     uint64_t wait_limit_ns;
 };
 
-__host__ __device__ inline int64_t pg_splits(int64_t L) { return (L + kPgSplit - 1) / kPgSplit; }
+__host__ __device__ inline int64_t pg_splits(int64_t L)
+{
+    return L <= 0 ? 0 : L <= kPgWhole ? 1 : (L + kPgSplit - 1) / kPgSplit;
+}
 
 // Length as the kernels use it: outside 0 .. max_len it is clamped (and reported by the first launch).
 __device__ __forceinline__ int pg_len(int L, int max_len)
@@ -164,8 +170,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int sg = (int)(it / n_kv), g = (int)(it - (uint32_t)sg * n_kv);
         const int b = warp_count_le(first, p.B, sg) - 1;
         const int split = sg - first[b], t0 = split * kPgSplit;
-        const int left = lens_s[b] - t0;
-        return {b, g, split, t0, left < kPgSplit ? left : kPgSplit};
+        const int L = lens_s[b], left = L - t0, most = L <= kPgWhole ? kPgWhole : kPgSplit;
+        return {b, g, split, t0, left < most ? left : most};
     };
 
     if (warp >= kPgWarps) {
@@ -176,61 +182,63 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const uint32_t pw = (uint32_t)(warp - kPgWarps);
         const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
         const int nb = kPgTile / p.box;                   // boxes per tile
-        constexpr int kRegs = kPgSplit / 32;              // boxes of an item per lane, at one token a box
-        int32_t page[kRegs], row[kRegs];
-        // Lane l holds boxes l, l + 32, ... of the item: their pages and the first row within.
-        auto look_up = [&](const Item &w, int32_t (&pg)[kRegs], int32_t (&rw)[kRegs]) {
-            const int boxes = (w.n + p.box - 1) / p.box;
-#pragma unroll
-            for (int r = 0; r < kRegs; ++r) {
-                const int k = lane + 32 * r;
-                pg[r] = 0;
-                rw[r] = 0;
-                if (32 * r < boxes && k < boxes) {
-                    const uint32_t t = (uint32_t)(w.t0 + k * p.box), c = t / (uint32_t)p.page_size;
-                    pg[r] = p.table[w.b * p.table_row + c];
-                    rw[r] = (int32_t)(t - c * (uint32_t)p.page_size);
-                }
+        const int chunk_tiles = 32 / nb;                  // tiles of a chunk: 32 boxes, one per lane
+        // A chunk of an item: its lane's box, the page it lies in and its first row there.
+        struct Chunk {
+            Item w;
+            uint32_t it;    // the item's number (>= items: none left)
+            int tile0;      // first tile of the chunk within the item
+            int32_t page, row;
+        };
+        auto look_up = [&](Chunk &c) {
+            const int k = c.tile0 * kPgTile + lane * p.box;  // token within the item
+            c.page = c.row = 0;
+            if (k < c.w.n) {
+                const uint32_t t = (uint32_t)(c.w.t0 + k), at = t / (uint32_t)p.page_size;
+                c.page = p.table[c.w.b * p.table_row + at];
+                c.row = (int32_t)(t - at * (uint32_t)p.page_size);
             }
+        };
+        auto enter = [&](Chunk &c, uint32_t it) {  // the first chunk of the next item with tokens, from item `it` on
+            for (c.it = it; c.it < items; c.it += gridDim.x) {
+                c.w = item(c.it);
+                if (c.w.n > 0) break;
+            }
+            c.tile0 = 0;
+            if (c.it < items) look_up(c);
         };
         uint32_t base = 0, mine = 0;  // the item's first tile number; tiles this warp has issued
         bool ok = true;
-        Item w{};
-        if (blockIdx.x < items) {
-            w = item(blockIdx.x);
-            look_up(w, page, row);
-        }
-        for (uint32_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
-            Item wn{};
-            int32_t page_n[kRegs], row_n[kRegs];
-            const bool more = it + gridDim.x < items;
-            if (more) {
-                wn = item(it + gridDim.x);
-                look_up(wn, page_n, row_n);
+        Chunk cur;
+        enter(cur, blockIdx.x);
+        while (ok && cur.it < items) {
+            // The next chunk's pages are looked up while this one's boxes are issued.
+            const int tiles = (cur.w.n + kPgTile - 1) / kPgTile, end = cur.tile0 + chunk_tiles;
+            Chunk next = cur;
+            if (end < tiles) {
+                next.tile0 = end;
+                look_up(next);
+            } else {
+                enter(next, cur.it + gridDim.x);
             }
-            const int boxes = (w.n + p.box - 1) / p.box, tiles = (w.n + kPgTile - 1) / kPgTile;
-            for (int j = (int)((pw - base) % kPgProducers); j < tiles; j += kPgProducers) {
+            const int boxes = (cur.w.n + p.box - 1) / p.box;
+            const uint32_t n0 = base + (uint32_t)cur.tile0;
+            for (int j = cur.tile0 + (int)((pw - n0) % kPgProducers); j < end && j < tiles; j += kPgProducers) {
                 const uint32_t num = base + (uint32_t)j, stage = num % C::kStages, use = num / C::kStages;
                 ok = __all_sync(0xffffffffu, wait_bounded(&empty[stage], (use & 1u) ^ 1u, abort_flag, p.status, lim));
                 if (!ok) break;
                 const int k0 = j * nb, cnt = boxes - k0 < nb ? boxes - k0 : nb;
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(cnt * p.box * D * 2 * 2));
                 __syncwarp();
-                const int r = k0 >> 5, x = lane - (k0 & 31);
-                int32_t pg = page[0], rw = row[0];
-#pragma unroll
-                for (int q = 1; q < kRegs; ++q)
-                    if (r == q) {
-                        pg = page[q];
-                        rw = row[q];
-                    }
+                const int x = lane - (j - cur.tile0) * nb;
                 if (x >= 0 && x < cnt) {
+                    int32_t pg = cur.page;
                     if (pg < 0 || pg >= p.pages) {  // no such page: recorded, and read as zeros (out of the map's range)
                         *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
                         pg = p.pages;
                     }
                     uint8_t *dst = smem + stage * C::kStageBytes + x * p.box * 128;
-                    const int c1 = p.heads_inner ? w.g : rw, c2 = p.heads_inner ? rw : w.g;
+                    const int c1 = p.heads_inner ? cur.w.g : cur.row, c2 = p.heads_inner ? cur.row : cur.w.g;
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_4d(dst + h * C::kHalfBytes, &tm_k, &full[stage], 64 * h, c1, c2, pg, policy);
@@ -240,15 +248,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
                 ++mine;
             }
-            base += (uint32_t)tiles;
-            if (more) {
-                w = wn;
-#pragma unroll
-                for (int r = 0; r < kRegs; ++r) {
-                    page[r] = page_n[r];
-                    row[r] = row_n[r];
-                }
-            }
+            if (next.it != cur.it) base += (uint32_t)tiles;
+            cur = next;
         }
         if (!ok && lane == 0) {
             // A wait ran out: let every copy this warp has issued land before shared memory goes away.
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
     } else {
         // ------------------------------------------------------------------ consumers
-        // Group grp takes the CTA's items grp, grp + 2, ...; its warp cw tiles cw and cw + 4 of each.  Tiles are
+        // Group grp takes the CTA's items grp, grp + 2, ...; its warp cw tiles cw, cw + 4, ... of each.  Tiles are
         // numbered across all of the CTA's items in the producer's order; tile number n is use n / kStages of stage
         // n % kStages.  A stage's uses are passed in order: once its previous use has been passed (slot_use, by
         // either group) its barrier is at most one phase from the one waited for, so a parity wait is exact.
@@ -476,82 +477,141 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
 }
 
-// Launch 2: grid (Hq, B), 256 threads.  The block's 1024 / D groups of D/4 lanes take the splits s, s +
-// groups, ... in ascending order, four columns a lane; the groups are then folded in order.
+// ---------------------------------------------------------------------------------------- launch 2
+// Folds the splits of each (sequence, query head).  Up to kPgSerial splits run in ascending order; more are taken
+// by 32 groups, group g splits g, g + 32, ..., folded in a fixed butterfly and then in order.  The cut depends on
+// the sequence's own number of splits, so both kernels below give a sequence the same bits.
 constexpr int kPgCombineThreads = 256;
+constexpr int kPgSerial = 32;
+constexpr int kPgAhead = 8;  // splits whose values a thread has in flight
 
+struct PgFold {
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __device__ __forceinline__ void add(float4 v, float2 ml, float ref)
+    {
+        const float f = ex2(ml.x - ref);  // 0 for the padding (maximum -inf)
+        l = __fmaf_rn(ml.y, f, l);
+        o.x = __fmaf_rn(v.x, f, o.x);
+        o.y = __fmaf_rn(v.y, f, o.y);
+        o.z = __fmaf_rn(v.z, f, o.z);
+        o.w = __fmaf_rn(v.w, f, o.w);
+    }
+    // Splits first, first + step, ... below n; lanes of a row hold four columns each.
+    __device__ __forceinline__ void run(const float2 *ml, const float4 *v, int row, int first, int step, int n, float ref)
+    {
+        for (int s0 = first; s0 < n; s0 += kPgAhead * step) {
+            float4 x[kPgAhead];
+            float2 w[kPgAhead];
+#pragma unroll
+            for (int k = 0; k < kPgAhead; ++k) {
+                const int s = s0 + k * step;
+                x[k] = s < n ? v[(int64_t)s * row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < kPgAhead; ++k) add(x[k], w[k], ref);
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *out) const
+    {
+        uint2 u;
+        u.x = pack_bf16(o.x / l, o.y / l);
+        u.y = pack_bf16(o.z / l, o.w / l);
+        *reinterpret_cast<uint2 *>(out) = u;
+    }
+};
+
+__device__ __forceinline__ float pg_warp_max(float m)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// No sequence has more than kPgSerial splits: a warp takes 128 / D (sequence, head) pairs.
 template <int D>
 __global__ void __launch_bounds__(kPgCombineThreads)
     paged_attention_combine_kernel(const float2 *__restrict__ part_ml, const float *__restrict__ part_o,
                                    const int32_t *__restrict__ lens, __nv_bfloat16 *__restrict__ out, int Hq, int S,
-                                   int max_len)
+                                   int max_len, int rows)
 {
-    constexpr int kLanes = D / 4, kGroups = kPgCombineThreads / kLanes, kAhead = 4;
-    __shared__ float red[kPgCombineThreads / 32], sl[kGroups];
-    __shared__ float4 so[kGroups][kLanes];
+    constexpr int kLanes = D / 4;
     griddep_wait();
     griddep_launch_dependents();
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, grp = tid / kLanes, c = tid % kLanes;
+    const int bh = (int)((blockIdx.x * (unsigned)kPgCombineThreads + threadIdx.x) / kLanes), c = threadIdx.x % kLanes;
+    const int n = bh < rows ? (int)pg_splits(pg_len(lens[bh / Hq], max_len)) : 0;
+    const float2 *ml = part_ml + (int64_t)bh * S;
+    float m = kNegInf;
+    for (int s = c; s < n; s += kLanes) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (n <= 1) return;  // written by launch 1, or no such row
+    PgFold f;
+    f.run(ml, reinterpret_cast<const float4 *>(part_o + (int64_t)bh * S * D) + c, kLanes, 0, 1, n, m == kNegInf ? 0.0f : m);
+    f.store(out + (int64_t)bh * D + 4 * c);
+}
+
+// Grid (D / 32, Hq, B): 8 lanes of four columns, 32 groups.
+template <int D>
+__global__ void __launch_bounds__(kPgCombineThreads)
+    paged_attention_combine_long_kernel(const float2 *__restrict__ part_ml, const float *__restrict__ part_o,
+                                        const int32_t *__restrict__ lens, __nv_bfloat16 *__restrict__ out, int Hq, int S,
+                                        int max_len)
+{
+    constexpr int kWarps = kPgCombineThreads / 32;
+    __shared__ float red[kWarps], sl[kWarps];
+    __shared__ float4 so[kWarps][8];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid / 8, c = tid % 8 + 8 * blockIdx.x;
+    const int h = blockIdx.y, b = blockIdx.z;
     const int n = (int)pg_splits(pg_len(lens[b], max_len));
     if (n <= 1) return;  // written by launch 1
     const int64_t bh = (int64_t)b * Hq + h;
     const float2 *ml = part_ml + bh * S;
     const float4 *po = reinterpret_cast<const float4 *>(part_o + bh * S * D) + c;
-    // The first values are on their way while the maximum (exact in any order) is found.
-    float4 v[kAhead];
-    float2 w[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        const int s = grp + k * kGroups;
-        v[k] = s < n ? po[(int64_t)s * kLanes] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
-    }
     float m = kNegInf;
     for (int s = tid; s < n; s += kPgCombineThreads) m = fmaxf(m, ml[s].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
+    m = pg_warp_max(m);
+    if (lane == 0) red[warp] = m;
     __syncthreads();
     m = red[0];
 #pragma unroll
-    for (int k = 1; k < kPgCombineThreads / 32; ++k) m = fmaxf(m, red[k]);
+    for (int k = 1; k < kWarps; ++k) m = fmaxf(m, red[k]);
     const float ref = m == kNegInf ? 0.0f : m;
-    float l = 0.0f;
-    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s0 = grp; s0 < n; s0 += kAhead * kGroups) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const float f = ex2(w[k].x - ref);  // 0 past the last split
-            l = __fmaf_rn(w[k].y, f, l);
-            r.x = __fmaf_rn(v[k].x, f, r.x);
-            r.y = __fmaf_rn(v[k].y, f, r.y);
-            r.z = __fmaf_rn(v[k].z, f, r.z);
-            r.w = __fmaf_rn(v[k].w, f, r.w);
+    PgFold f;
+    if (n <= kPgSerial) {
+        if (grp == 0) {
+            f.run(ml, po, D / 4, 0, 1, n, ref);
+            f.store(out + bh * D + 4 * c);
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int s = s0 + (kAhead + k) * kGroups;
-            v[k] = s < n ? po[(int64_t)s * kLanes] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
-        }
+        return;
     }
-    so[grp][c] = r;
-    if (c == 0) sl[grp] = l;
+    f.run(ml, po, D / 4, grp, kPgCombineThreads / 8, n, ref);
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        f.l = __fadd_rn(f.l, __shfl_xor_sync(0xffffffffu, f.l, o));
+        f.o.x = __fadd_rn(f.o.x, __shfl_xor_sync(0xffffffffu, f.o.x, o));
+        f.o.y = __fadd_rn(f.o.y, __shfl_xor_sync(0xffffffffu, f.o.y, o));
+        f.o.z = __fadd_rn(f.o.z, __shfl_xor_sync(0xffffffffu, f.o.z, o));
+        f.o.w = __fadd_rn(f.o.w, __shfl_xor_sync(0xffffffffu, f.o.w, o));
+    }
+    if (lane < 8) so[warp][lane] = f.o;
+    if (lane == 0) sl[warp] = f.l;
     __syncthreads();
-    if (tid < kLanes) {
-        r = so[0][c];
-        l = sl[0];
-        for (int g = 1; g < kGroups; ++g) {
-            l = __fadd_rn(l, sl[g]);
-            r.x = __fadd_rn(r.x, so[g][c].x);
-            r.y = __fadd_rn(r.y, so[g][c].y);
-            r.z = __fadd_rn(r.z, so[g][c].z);
-            r.w = __fadd_rn(r.w, so[g][c].w);
+    if (tid < 8) {
+        f.l = sl[0];
+        f.o = so[0][tid];
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 v = so[w][tid];
+            f.l = __fadd_rn(f.l, sl[w]);
+            f.o.x = __fadd_rn(f.o.x, v.x);
+            f.o.y = __fadd_rn(f.o.y, v.y);
+            f.o.z = __fadd_rn(f.o.z, v.z);
+            f.o.w = __fadd_rn(f.o.w, v.w);
         }
-        uint2 u;
-        u.x = pack_bf16(r.x / l, r.y / l);
-        u.y = pack_bf16(r.z / l, r.w / l);
-        *reinterpret_cast<uint2 *>(out + bh * D + 4 * c) = u;
+        f.store(out + bh * D + 4 * c);
     }
 }
 

@@ -85,19 +85,19 @@ def test_paged_attention_refusals(lib):
         assert attend(c=cache(**kw)) == status, kw
     for bad in (dict(B=-1), dict(Hq=0), dict(Hq=7), dict(max_len=0), dict(mp=0), dict(max_len=129), dict(q=NULL),
                 dict(table=NULL), dict(lens=NULL), dict(out=NULL), dict(qs=512), dict(ts=7),
-                dict(mp=100, ts=100, max_len=300, scratch=NULL), dict(mp=100, ts=100, max_len=300, nbytes=1000)):
+                dict(mp=100, ts=100, max_len=600, scratch=NULL), dict(mp=100, ts=100, max_len=600, nbytes=1000)):
         assert attend(**bad) == I, bad
     for bad in (dict(c=cache(head_dim=96, head_stride=96)), dict(Hq=34), dict(B=65536), dict(Hq=65536),
                 dict(mp=1 << 31, ts=1 << 31), dict(mp=1 << 30, ts=1 << 30, max_len=(1 << 31) - 2)):
         assert attend(**bad) == U, bad
     for bad in (dict(q=FAKE + 2), dict(out=FAKE + 8), dict(lens=FAKE + 2), dict(table=FAKE + 1), dict(qs=1028),
-                dict(mp=100, ts=100, max_len=300, scratch=FAKE + 4)):
+                dict(mp=100, ts=100, max_len=600, scratch=FAKE + 4)):
         assert attend(**bad) == A, bad
     assert attend(B=0, q=NULL) == OK
     need = lib.bi_paged_decode_attention_scratch_bytes
-    assert need(4, 8, 128, 256) == 0 and need(0, 8, 128, 999) == 0
-    assert need(4, 8, 128, 257) == 4 * 8 * 2 * (128 * 4 + 8)
-    assert need(5000, 8, 128, 257) == need(2048, 8, 128, 257)  # sequences are taken 2048 at a time
+    assert need(4, 8, 128, 512) == 0 and need(0, 8, 128, 999) == 0
+    assert need(4, 8, 128, 513) == 4 * 8 * 3 * (128 * 4 + 8)
+    assert need(5000, 8, 128, 513) == need(2048, 8, 128, 513)  # sequences are taken 2048 at a time
 
 
 def test_token_logprobs_refusals(lib):

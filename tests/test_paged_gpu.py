@@ -5,7 +5,7 @@ Attention tolerance: with p the weights, A = sum_t p_t |v_t| and s_max = max_t s
   |out - ref| <= 2^-8 |ref| + A (2 (D + 4) 2^-24 s_max + 2^-16 + (2 n_t) 2^-24):
 a score's D fp32 products and its scaling are off by (D + 4) 2^-24 of s_max and enter numerator and denominator; the weights
 are two bf16 terms (2^-17 of each, numerator against the denominator's fp32 ones) through ex2 (2^-22); sums run over 32
-tokens, 8 tiles and the splits (n_t = 64 + splits terms in a chain, in both); then one rounding to bf16.
+tokens, up to 16 tiles and the splits (n_t = 64 + splits terms in a chain, in both); then one rounding to bf16.
 """
 import pytest
 import torch
@@ -88,7 +88,7 @@ def close(o, ref, bound):
 @pytest.mark.parametrize("D", [128, 64])
 @pytest.mark.parametrize("page", [16, 1, 2, 5, 8, 24, 32, 48, 64, 256])
 def test_attention_page_sizes(page, D):
-    lens = [1, 31, 32, 33, 255, 256, 257, 0, 700]
+    lens = [1, 31, 32, 33, 255, 256, 257, 0, 700, 511, 512, 513, 768]
     q, kc, vc, table, sl = run_attend(100 + page, lens, 8, 2, D, page)
     o = bi.bi_paged_decode_attention(q, kc, vc, table, sl)
     close(o, *attend_definition(q, kc, vc, table, lens, D ** -0.5))
@@ -144,19 +144,24 @@ def test_attention_does_not_depend_on_batch_pages_or_max_len():
     assert same_bits(bi.bi_paged_decode_attention(q, k2, v2, t2, sl), want)
 
 
-def test_attention_long_sequence_and_many_splits():
-    lens = [70001, 300]
-    q, kc, vc, table, sl = run_attend(91, lens, 4, 1, 128, 64)
-    close(bi.bi_paged_decode_attention(q, kc, vc, table, sl), *attend_definition(q, kc, vc, table, lens, 128 ** -0.5))
+@pytest.mark.parametrize("D", [128, 64])
+def test_attention_long_sequence_and_many_splits(D):
+    """More than 32 splits are folded by groups, up to 32 in order, whichever the longest of the call asks for."""
+    lens = [70001, 300, 8192, 8193, 0, 600]
+    q, kc, vc, table, sl = run_attend(91, lens, 4, 1, D, 64)
+    o = bi.bi_paged_decode_attention(q, kc, vc, table, sl)
+    close(o, *attend_definition(q, kc, vc, table, lens, D ** -0.5))
+    for i in (1, 2, 3, 5):
+        assert same_bits(bi.bi_paged_decode_attention(q[i:i + 1], kc, vc, table[i:i + 1], sl[i:i + 1], max_len=lens[i]), o[i:i + 1])
 
 
 def test_attention_more_sequences_than_one_launch_takes():
-    lens = [1 + (i * 37) % 300 for i in range(2100)]
+    lens = [1 + (i * 37) % 300 for i in range(2098)] + [700, 1300]
     q, kc, vc, table, sl = run_attend(92, lens, 2, 1, 64, 16)
     o = bi.bi_paged_decode_attention(q, kc, vc, table, sl)
     close(o, *attend_definition(q, kc, vc, table, lens, 0.125))
     for i in (0, 2047, 2048, 2099):
-        assert same_bits(bi.bi_paged_decode_attention(q[i:i + 1], kc, vc, table[i:i + 1], sl[i:i + 1], max_len=300), o[i:i + 1])
+        assert same_bits(bi.bi_paged_decode_attention(q[i:i + 1], kc, vc, table[i:i + 1], sl[i:i + 1], max_len=int(sl[i])), o[i:i + 1])
 
 
 def test_attention_offsets_beyond_32_bits():
