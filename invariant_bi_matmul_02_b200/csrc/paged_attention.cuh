@@ -15,7 +15,7 @@
 // numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
 // how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
 // other's arithmetic and loads.  The producers fill a ring of tiles (K and V of 32 tokens: 16 KB at
-// head size 128, 12 tiles; 8 KB at 64, 24 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
+// head size 128, 8 tiles; 8 KB at 64, 20 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
 // entries, each within one page and completing on the tile's mbarrier.  The lanes look pages up one chunk of
 // 32 boxes ahead and each issues its own box.  Four producer warps issue alternate tiles: one warp needs about
 // 1000 cycles a tile in pages of 16 (wait, barrier, 8 copies), more than a tile takes to arrive.
@@ -45,7 +45,6 @@ constexpr int kPgSplit = 256;                    // tokens per split: two tiles 
 constexpr int kPgWhole = 512;                    // a sequence of up to this many tokens is one split
 constexpr int kPgProducers = 4;                  // producer warps
 constexpr int kPgThreads = 32 * (kPgWarps + kPgProducers);
-constexpr int kPgFold = 4;                       // query heads folded at a time
 constexpr int kPgSeqs = 2048;                    // sequences per launch (their prefix sums are in shared memory)
 
 template <int D>
@@ -54,11 +53,11 @@ struct PgShape {
     static constexpr int kHalfBytes = kPgTile * 128;        // one half of a tile's K or V
     static constexpr int kKBytes = kHalves * kHalfBytes;    // K (or V) of a tile
     static constexpr int kStageBytes = 2 * kKBytes;
-    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    static constexpr int kStages = D == 64 ? 20 : 8;        // 160 or 128 KB: what the fold's buffers leave, by fours
     static constexpr int kORow = D + 4;                     // floats between heads of a warp's sums: no bank conflicts
-    static constexpr int kOBytes = kPgWarps * kPgFold * kORow * 4;
+    static constexpr int kOFloats = kPgWarps * 8 * kORow;   // one buffer of the warps' sums, eight heads
     static_assert(kStages % kPgProducers == 0, "a stage is always filled by the same producer warp");
-    static constexpr int kSmem = kStages * kStageBytes + kOBytes + 1024;  // + alignment slack
+    static constexpr int kSmem = kStages * kStageBytes + 2 * kOFloats * 4 + 1024;  // + alignment slack
 };
 
 struct PgParams {
@@ -107,9 +106,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     using C = PgShape<D>;
     extern __shared__ uint8_t pg_raw[];
     uint8_t *smem = pg_raw + ((1024u - (smem_addr(pg_raw) & 1023u)) & 1023u);
-    float *so_all = reinterpret_cast<float *>(smem + C::kStages * C::kStageBytes);  // [warp][kPgFold heads][kORow]
+    float *so_all = reinterpret_cast<float *>(smem + C::kStages * C::kStageBytes);  // [2][warp][8 heads][kORow]
     __shared__ uint64_t full[C::kStages], empty[C::kStages];
-    __shared__ float red_m[kPgWarps][8 * NT], red_l[kPgWarps][8 * NT];
+    __shared__ float red_m[2][kPgWarps][8], red_l[2][kPgWarps][8];
     __shared__ int32_t first[kPgSeqs + 1];  // global number of each sequence's first split
     __shared__ int32_t lens_s[kPgSeqs];
     __shared__ int32_t warp_total[kPgThreads / 32];
@@ -166,10 +165,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     struct Item {
         int b, g, split, t0, n;  // n tokens from t0 on
     };
+    // Items come in ascending order: the sequence is searched from the last one on, 32 at a time.
+    int b = 0, first_b = 0;
     auto item = [&](uint32_t it) -> Item {
         const int sg = (int)(it / n_kv), g = (int)(it - (uint32_t)sg * n_kv);
-        const int b = warp_count_le(first, p.B, sg) - 1;
-        const int split = sg - first[b], t0 = split * kPgSplit;
+        int passed;
+        do {
+            const int v = b + 1 + lane < p.B ? first[b + 1 + lane] : 0x7fffffff;
+            passed = __popc(__ballot_sync(0xffffffffu, v <= sg));
+            if (passed > 0) first_b = __shfl_sync(0xffffffffu, v, passed - 1);
+            b += passed;
+        } while (passed == 32);
+        const int split = sg - first_b, t0 = split * kPgSplit;
         const int L = lens_s[b], left = L - t0, most = L <= kPgWhole ? kPgWhole : kPgSplit;
         return {b, g, split, t0, left < most ? left : most};
     };
@@ -271,8 +278,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const int gid = lane >> 2, tig = lane & 3;
         uint32_t base = 0, local = 0;
         bool alive = true;
-        float *so_grp = so_all + grp * kPgGroupWarps * kPgFold * C::kORow, *so = so_grp + cw * kPgFold * C::kORow;
-        float(*gm)[8 * NT] = red_m + grp * kPgGroupWarps, (*gl)[8 * NT] = red_l + grp * kPgGroupWarps;
+        const int w0 = grp * kPgGroupWarps;  // the group's first warp
+        int buf = 0;
         for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
             const Item w = item(it);
             const int tiles = (w.n + kPgTile - 1) / kPgTile;
@@ -414,9 +421,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     if (lane == 0) mbar_arrive(&empty[stage]);
                 }
             }
-            // ---- fold the warps in order, kPgFold heads at a time through shared memory
+            // ---- fold the warps in order through shared memory, eight heads at a time.  Two buffers: a warp that
+            // writes one has passed the barrier behind which the other was read.
+            const bool last = first[w.b + 1] - first[w.b] == 1;  // the sequence's only split
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const int heads = p.G - 8 * nt < 8 ? p.G - 8 * nt : 8;
+                float(*gm)[8] = red_m[buf] + w0, (*gl)[8] = red_l[buf] + w0;
+                float *so_grp = so_all + buf * C::kOFloats + w0 * 8 * C::kORow, *so = so_grp + cw * 8 * C::kORow;
+                buf ^= 1;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float v = l[nt][c];
@@ -424,28 +437,21 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
                     if (gid == 0) {
-                        gm[cw][8 * nt + 2 * tig + c] = m[nt][c];
-                        gl[cw][8 * nt + 2 * tig + c] = v;
+                        gm[cw][2 * tig + c] = m[nt][c];
+                        gl[cw][2 * tig + c] = v;
                     }
                 }
-            const bool last = first[w.b + 1] - first[w.b] == 1;  // the sequence's only split
-#pragma unroll
-            for (int round = 0; round < 8 * NT / kPgFold; ++round) {
-                const int h0 = kPgFold * round, nt = h0 / 8;
-                const int heads = p.G - h0 < kPgFold ? p.G - h0 : kPgFold;
-                if (heads <= 0) break;
-                const int hl = 8 * nt + 2 * tig - h0;  // this thread's heads are hl and hl + 1 of the round
-                if (cw < warps && hl >= 0 && hl < heads) {
+                if (cw < warps) {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (hl + (e & 1) < heads)
-                                so[(hl + (e & 1)) * C::kORow + 16 * mt + gid + 8 * (e >> 1)] = o[nt][mt][e];
+                            if (2 * tig + (e & 1) < heads)
+                                so[(2 * tig + (e & 1)) * C::kORow + 16 * mt + gid + 8 * (e >> 1)] = o[nt][mt][e];
                 }
                 consumers_sync(1 + grp);
                 for (int i = ct; i < heads * (D / 4); i += 32 * kPgGroupWarps) {
-                    const int hl = i / (D / 4), d = 4 * (i % (D / 4)), h = h0 + hl;
+                    const int h = i / (D / 4), d = 4 * (i % (D / 4));
                     float mx = gm[0][h];
                     for (int t = 1; t < warps; ++t) mx = fmaxf(mx, gm[t][h]);
                     const float ref = mx == kNegInf ? 0.0f : mx;
@@ -453,14 +459,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     for (int t = 0; t < warps; ++t) {
                         const float f = ex2(gm[t][h] - ref);
-                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * kPgFold + hl) * C::kORow + d);
+                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * 8 + h) * C::kORow + d);
                         sum = __fmaf_rn(gl[t][h], f, sum);
                         r.x = __fmaf_rn(v.x, f, r.x);
                         r.y = __fmaf_rn(v.y, f, r.y);
                         r.z = __fmaf_rn(v.z, f, r.z);
                         r.w = __fmaf_rn(v.w, f, r.w);
                     }
-                    const int64_t bh = (int64_t)w.b * p.Hq + head0 + h;
+                    const int64_t bh = (int64_t)w.b * p.Hq + head0 + 8 * nt + h;
                     if (last) {
                         uint2 u;
                         u.x = pack_bf16(r.x / sum, r.y / sum);
@@ -471,7 +477,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         if (d == 0) p.part_ml[bh * p.S + w.split] = make_float2(mx, sum);
                     }
                 }
-                consumers_sync(1 + grp);
             }
         }
     }
