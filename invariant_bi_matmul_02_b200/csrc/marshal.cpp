@@ -312,9 +312,20 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
     const bool scored = a[1] != Py_None;
     const void *tok = scored ? ptr(vec(a[1], "tokens", at::kInt, M, dev)) : nullptr;
     const float scale = (float)number(a[3]);
-    const Tensor lp = scored ? empty({M}, at::kFloat, dev) : Tensor(), h = empty({M}, at::kFloat, dev),
-                 lse = empty({M}, at::kFloat, dev), tl = empty({M, top}, at::kFloat, dev),
-                 tt = empty({M, top}, at::kInt, dev);
+    // One allocation holds the five results (each M or M * top four-byte values, a multiple of 16 bytes apart).
+    auto room = [](int64_t values) { return (values + 3) / 4 * 4; };
+    const Tensor buffer = empty({3 * room(M) + 2 * room(M * top)}, at::kFloat, dev);
+    int64_t at_value = 0;
+    auto part = [&](at::IntArrayRef sizes, at::ScalarType type) {
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        t.unsafeGetTensorImpl()->set_storage_offset(at_value);
+        at_value += room(t.numel());
+        return t;
+    };
+    const Tensor lp = part({M}, at::kFloat), h = part({M}, at::kFloat), lse = part({M}, at::kFloat),
+                 tl = part({M, top}, at::kFloat), tt = part({M, top}, at::kInt);
     void *s = stream_of(a[4], dev);
     BI_CALL("bi_token_logprobs", p_token_logprobs, ptr(x), ld, x.scalar_type() == at::kBFloat16 ? BI_BF16 : BI_F32,
             static_cast<const int32_t *>(tok), scale, top, scored ? static_cast<float *>(ptr(lp)) : nullptr,

@@ -259,6 +259,7 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
         s.range[0][warp] = low_of_warp;
         s.range[1][warp] = top_of_warp;
     }
+    for (int j = tid; j < kTlKeys; j += kTlThreads) s.keys[j] = 0;
     if (tid == 0) s.n_columns = s.n_groups = s.n_keys = 0;
     __syncthreads();
     // Invariant: at least `top` threads reach lo (or lo is the least of all: every group is a candidate), fewer reach hi.
@@ -295,7 +296,7 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
     __syncthreads();
     const int n_groups = s.n_groups;
     if (n_groups > kTlGroups) return false;
-    constexpr int kBatch = 4;  // elements a thread has in flight
+    constexpr int kBatch = 6;  // elements a thread has in flight
     for (int i0 = tid; i0 - tid < n_groups * kGroup; i0 += kBatch * kTlThreads) {
         float v[kBatch];
         int e[kBatch];
@@ -319,7 +320,9 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
     if (tid < n) {
         const uint64_t key = s.keys[tid];
         int place = 0;
-        for (int j = 0; j < n; ++j) place += s.keys[j] > key;
+        for (int j = 0; j < n; j += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) place += s.keys[j + k] > key;  // 0 past the n-th
         if (place < p.top) out[place] = key;
     }
     return true;
