@@ -1194,9 +1194,13 @@ bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const 
     p.top_logprobs = top_logprobs;
     p.top_tokens = top_tokens;
     p.status = dev->status;
-    // Blocks that share a row: as many as keep all rows resident at once, none idle.
+    // Blocks that share a row: as many as leave the GPU 2 blocks an SM (top 8 of 64 rows of 151936 bf16: 10.9 us with
+    // clusters of 4, 13.2 with 8, which fill it), or 3.5 where rows are longer than 384 KB and each block's share
+    // counts for more (160 rows of 151936 fp32: 26.0 us with clusters of 2, 32.8 alone).  Never all 4:
+    // clusters do not pack, and a few rows would run after the rest (148 rows of bf16: 21.2 against 16.1 us).
+    const int64_t row_bytes = V * (bf16 ? 2 : 4), most = (row_bytes > 384 * 1024 ? 7 : 4) * (int64_t)dev->sms / 2;
     p.cluster = bi::kTlMaxCluster;
-    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > (int64_t)bi::kTlBlocks * dev->sms)) p.cluster /= 2;
+    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > most)) p.cluster /= 2;
     const size_t smem = token_logprobs_smem((p.pieces + p.cluster - 1) / p.cluster, top_k);
     const bool vec = aligned16(x) && (M == 1 || ldx % (bf16 ? 8 : 4) == 0);
     void (*kernel)(bi::TlParams) = bf16 ? (vec ? bi::token_logprobs_kernel<true, true> : bi::token_logprobs_kernel<true, false>)
