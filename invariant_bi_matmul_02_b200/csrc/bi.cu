@@ -515,11 +515,21 @@ bi_status split_launches(bool bf16, dim3 grid, cudaStream_t s, const uint8_t *xb
                          static_cast<const float2 *>(part), y, V);
 }
 
-// Whether heads of `n` strided [.., heads, D] tensors can be moved in 16-byte pieces of W elements.
-inline bool rope_pieces(int64_t W, int64_t D, int64_t R) { return (R / 2) % W == 0 && (D - R) % W == 0; }
-inline bool strided_pieces(int64_t W, const void *p, int64_t s0, int64_t s1)
+// Whether the heads of a strided [.., heads, D] tensor can be moved in pieces of W entries of `entry` bytes.
+inline bool strided_pieces(int64_t W, int64_t entry, const void *p, int64_t s0, int64_t s1)
 {
-    return aligned16(p) && s0 % W == 0 && s1 % W == 0;
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(W * entry - 1)) == 0 && s0 % W == 0 && s1 % W == 0;
+}
+
+// The widest piece (in bytes) that entries first .. first + n - 1 of every head can be copied in, between tensors
+// that `fits` (pieces of W entries) accepts; 0 for no entries.
+template <typename Fits>
+int copy_piece(int64_t first, int64_t n, int64_t entry, Fits fits)
+{
+    if (n == 0) return 0;
+    for (int64_t W = 16 / entry; W > 1; W /= 2)
+        if (first % W == 0 && n % W == 0 && fits(W)) return (int)(W * entry);
+    return (int)entry;
 }
 
 // Warps that share a token's heads in the rotation kernels: one where the tokens alone fill the GPU (the
@@ -532,8 +542,9 @@ inline int rope_shares(int64_t T, int64_t steps, int sms)
 }
 inline int64_t rope_steps(int64_t H, int64_t D, int64_t R, int64_t W)
 {
-    const int64_t units = R / (2 * W) + (D - R) / W, heads = units < 32 ? 32 / units : 1;
-    return (H + heads - 1) / heads;
+    const int64_t units = R / (2 * W), heads = units > 0 && units < 32 ? 32 / units : 1;
+    const int64_t turned = units > 0 ? (H + heads - 1) / heads : 0, copied = H * (D - R) / (32 * bi::kRopeCopies);
+    return turned > copied ? turned : copied > 0 ? copied : 1;
 }
 
 template <typename E, int W>
@@ -948,13 +959,21 @@ bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, 
     p.R = (int32_t)R;
     p.scale = scale;
     p.inverse = inverse ? 1 : 0;
-    const int64_t W = bf16 ? 8 : 4;
-    const bool pieces = rope_pieces(W, D, R) && strided_pieces(W, x, xt, xh) && strided_pieces(W, y, yt, yh);
+    // Pieces of 16 bytes, two entries or one, as sizes, strides and addresses allow (8284 tokens of 19 heads of 192, 74
+    // entries turned: 58 us by single entries; 20 turned: 38 by twos).
+    const int64_t entry = bf16 ? 2 : 4;
+    auto strided = [&](int64_t W) { return strided_pieces(W, entry, x, xt, xh) && strided_pieces(W, entry, y, yt, yh); };
+    auto fits = [&](int64_t W) { return R / 2 % W == 0 && strided(W); };
+    p.copy_piece = x == y ? 0 : copy_piece(R, D - R, entry, strided);
     const bool half = layout == BI_ROPE_HALF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (bf16)
-        return pieces ? launch_rope<__nv_bfloat16, 8>(p, half, dev->sms, s) : launch_rope<__nv_bfloat16, 1>(p, half, dev->sms, s);
-    return pieces ? launch_rope<float, 4>(p, half, dev->sms, s) : launch_rope<float, 1>(p, half, dev->sms, s);
+        return fits(8)   ? launch_rope<__nv_bfloat16, 8>(p, half, dev->sms, s)
+               : fits(2) ? launch_rope<__nv_bfloat16, 2>(p, half, dev->sms, s)
+                         : launch_rope<__nv_bfloat16, 1>(p, half, dev->sms, s);
+    return fits(4)   ? launch_rope<float, 4>(p, half, dev->sms, s)
+           : fits(2) ? launch_rope<float, 2>(p, half, dev->sms, s)
+                     : launch_rope<float, 1>(p, half, dev->sms, s);
 }
 
 bi_status bi_rope_freqs(int64_t R, double theta, bi_rope_kind kind, const double *params, int64_t n_params,
@@ -1069,12 +1088,18 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
     p.max_pages = (int32_t)max_pages;
     p.scale = scale;
     p.status = dev->status;
-    const bool pieces = rope_pieces(8, D, R) && strided_pieces(8, k, p.k_token, p.k_head) &&
-                        strided_pieces(8, v, p.v_token, p.v_head) && strided_pieces(8, q, qt, qh) &&
-                        strided_pieces(8, q_out, qot, qoh);
+    auto turned = [&](int64_t W) {  // the cache's strides and addresses fit any piece
+        return strided_pieces(W, 2, k, p.k_token, p.k_head) && strided_pieces(W, 2, q, qt, qh) &&
+               strided_pieces(W, 2, q_out, qot, qoh);
+    };
+    auto fits = [&](int64_t W) { return R / 2 % W == 0 && turned(W); };
+    p.rest_piece = copy_piece(R, D - R, 2, turned);
+    p.v_piece = copy_piece(0, D, 2, [&](int64_t W) { return strided_pieces(W, 2, v, p.v_token, p.v_head); });
     const bool half = layout == BI_ROPE_HALF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return pieces ? launch_append<8>(p, half, dev->sms, s) : launch_append<1>(p, half, dev->sms, s);
+    return fits(8)   ? launch_append<8>(p, half, dev->sms, s)
+           : fits(2) ? launch_append<2>(p, half, dev->sms, s)
+                     : launch_append<1>(p, half, dev->sms, s);
 }
 
 size_t bi_paged_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len)

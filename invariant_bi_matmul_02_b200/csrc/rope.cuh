@@ -11,9 +11,10 @@
 // Bound by memory for many tokens and by latency for few.  A warp takes a token (or a share of its heads
 // where there are few tokens): it works out the token's R/2 sines and cosines once, into its own piece of
 // shared memory, and its lanes keep a fixed place in the head while they walk the heads.  A lane's unit
-// is W entries a and their W partners b (16-byte pieces where sizes, strides and addresses allow it, single
-// entries otherwise; the arithmetic is the same), and kRopeUnits heads' loads are in flight before
-// the first angle is needed.
+// is W entries a and their W partners b (16-byte pieces where sizes, strides and addresses allow it, else two
+// entries or one; the arithmetic is the same).  A lane's next head is on its way while one is turned, and
+// the first is before the angles are worked out.  Entries that are only copied are moved apart from the
+// pairs, in the widest pieces that they allow.
 #pragma once
 
 #include <cstdint>
@@ -28,10 +29,9 @@ constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 6;      // resident per SM, a bound on registers
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 16 KB
-constexpr int kRopeUnits = 2;      // a lane's buffers: one head is turned while the others are on their way
 constexpr int kRopeCopies = 4;     // value pieces a lane has in flight
 
-// W consecutive entries as they sit in memory: 16 bytes, or one entry (W = 1).
+// W consecutive entries as they sit in memory: 16 bytes, two entries or one.
 template <typename E, int W>
 struct alignas(16) Piece {
     uint32_t w[4];
@@ -40,6 +40,19 @@ template <typename E>
 struct Piece<E, 1> {
     E e;
 };
+template <typename E>
+struct alignas(2 * sizeof(E)) Piece<E, 2> {
+    E e[2];
+};
+
+// A lane's buffers: one head is turned while the others are on their way.  More for smaller pieces, as registers
+// allow (8284 tokens of 19 heads of 192: single bf16 entries 85 us with 4, 116 with 2; pairs of them 73 with 2, 108
+// with 4; pairs of fp32 entries 37 with 6, 46 with 2; 16-byte pieces of 8192 x 40 x 128 31.4 with 2, 32.5 with 3).
+template <typename E, int W>
+__host__ __device__ constexpr int rope_buffers()
+{
+    return W == 1 ? 4 : W == 2 && sizeof(E) == 4 ? 6 : 2;
+}
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -89,6 +102,15 @@ __device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const 
         const float x = to_f32(a.e), y = to_f32(b.e);
         from_f32(__fmaf_rn(x, t.c[0], __fmul_rn(y, t.n[0])), a.e);
         from_f32(__fmaf_rn(y, t.c[0], __fmul_rn(x, t.s[0])), b.e);
+    } else if constexpr (W == 2) {
+        E &x0 = a.e[0], &x1 = HALF ? a.e[1] : b.e[0], &y0 = HALF ? b.e[0] : a.e[1], &y1 = b.e[1];
+        uint64_t x = f2_pack(to_f32(x0), to_f32(x1)), y = f2_pack(to_f32(y0), to_f32(y1));
+        t.turn2(0, x, y);
+        const float2 u = f2_unpack(x), v = f2_unpack(y);
+        from_f32(u.x, x0);
+        from_f32(u.y, x1);
+        from_f32(v.x, y0);
+        from_f32(v.y, y1);
     } else if constexpr (W == 8 && HALF) {  // bf16: a word holds entries 2j and 2j + 1
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -124,34 +146,20 @@ __device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const 
     }
 }
 
-// A lane's place in the heads its warp walks.  A head has R/2W units of pairs and then (D - R)/W single
-// pieces that are copied; 32 / units heads are taken at a time (or one head 32 units at a time).
-template <int W, bool HALF>
+// A lane's place in the heads its warp walks: a head has R/2W units; 32 / units heads are taken at a time (or one
+// head 32 units at a time).
+template <int W>
 struct RopeLane {
     int units, heads;  // units per head; heads the warp takes at a time
     int head, unit;    // this lane's first head and unit (unit >= units: the lane idles)
-    __device__ __forceinline__ RopeLane(int D, int R)
+    __device__ __forceinline__ explicit RopeLane(int R)
     {
         const int lane = threadIdx.x & 31;
-        units = R / (2 * W) + (D - R) / W;
-        heads = units < 32 ? 32 / units : 1;
-        head = units < 32 ? lane / units : 0;
+        units = R / (2 * W);
+        heads = units > 0 && units < 32 ? 32 / units : 1;
+        head = units > 0 && units < 32 ? lane / units : 0;
         unit = lane - head * units;
         if (head >= heads) unit = units;
-    }
-    // Entry offsets of unit u's two pieces (b < 0: one piece, copied) and its first pair.
-    static __device__ __forceinline__ void place(int u, int R, int &a, int &b, int &pair)
-    {
-        const int np = R / (2 * W);
-        if (u < np) {
-            pair = u * W;
-            a = HALF ? u * W : 2 * u * W;
-            b = HALF ? R / 2 + u * W : a + W;
-        } else {
-            pair = 0;
-            a = R + (u - np) * W;
-            b = -1;
-        }
     }
 };
 
@@ -162,51 +170,47 @@ __device__ __forceinline__ void rope_angles(float *cs, const double *inv_freq, i
     __syncwarp();
 }
 
-// Walks heads 0 .. H-1 of one token, every `shares`-th group of them from group `group` on: src to the
+// Turns heads 0 .. H-1 of one token, every `shares`-th group of them from group `group` on: src to the
 // place that dst() gives.  ready() is called once the first loads are in flight and before cs or dst() is
-// needed; false ends the walk.  copy: whether single pieces are written (not when y is x).
+// needed; false ends the walk.
 template <typename E, int W, bool HALF, typename Ready, typename Dst>
-__device__ __forceinline__ bool rope_walk(const RopeLane<W, HALF> &me, const E *src, int64_t src_head, int64_t dst_head,
-                                          int H, int R, int group, int shares, const float *cs, bool copy, Ready ready,
-                                          Dst dst)
+__device__ __forceinline__ bool rope_walk(const RopeLane<W> &me, const E *src, int64_t src_head, int64_t dst_head, int H,
+                                          int R, int group, int shares, const float *cs, Ready ready, Dst dst)
 {
     const int h_step = me.heads * shares, half = R / 2;
     const int64_t src_step = h_step * src_head, dst_step = h_step * dst_head;
     for (int u0 = 0; u0 < me.units; u0 += 32) {
         const int u = me.unit + u0;
-        const bool on = u < me.units;
-        int ea, eb, pair;
-        RopeLane<W, HALF>::place(u, R, ea, eb, pair);
-        // Heads left for this lane and for the warp's first lane (the loop's bound).
+        const int ea = HALF ? u * W : 2 * u * W, eb = HALF ? half + u * W : ea + W;
+        // Heads left for this lane, and for the warp's first lane (the loop's bound).
         const int h = me.head + group * me.heads;
-        int left = on && h < H ? (H - h + h_step - 1) / h_step : 0;
+        int left = u < me.units && h < H ? (H - h + h_step - 1) / h_step : 0;
         int turns = group * me.heads < H ? (H - group * me.heads + h_step - 1) / h_step : 0;
         if (turns == 0) continue;
         const E *from = src + h * src_head;
-        Piece<E, W> a[kRopeUnits], b[kRopeUnits];
+        constexpr int kBuffers = rope_buffers<E, W>();
+        Piece<E, W> a[kBuffers], b[kBuffers];
         auto load = [&](int k, bool some) {
             if (some) {
                 a[k] = *reinterpret_cast<const Piece<E, W> *>(from + ea);
-                if (eb >= 0) b[k] = *reinterpret_cast<const Piece<E, W> *>(from + eb);
+                b[k] = *reinterpret_cast<const Piece<E, W> *>(from + eb);
             }
             from += src_step;
         };
 #pragma unroll
-        for (int k = 0; k + 1 < kRopeUnits; ++k) load(k, left > k);
+        for (int k = 0; k + 1 < kBuffers; ++k) load(k, left > k);
         if (!ready()) return false;
         RopeTurn<W> turn;
-        if (on && eb >= 0) turn.load(cs, half, pair);
+        if (u < me.units) turn.load(cs, half, u * W);
         E *to = dst() + h * dst_head;
         while (turns > 0) {
 #pragma unroll
-            for (int k = 0; k < kRopeUnits; ++k) {
-                load((k + kRopeUnits - 1) % kRopeUnits, left > kRopeUnits - 1);
+            for (int k = 0; k < kBuffers; ++k) {
+                load((k + kBuffers - 1) % kBuffers, left > kBuffers - 1);
                 if (left > 0) {
-                    if (eb >= 0) {
-                        rope_unit<E, W, HALF>(a[k], b[k], turn);
-                        *reinterpret_cast<Piece<E, W> *>(to + eb) = b[k];
-                    }
-                    if (eb >= 0 || copy) *reinterpret_cast<Piece<E, W> *>(to + ea) = a[k];
+                    rope_unit<E, W, HALF>(a[k], b[k], turn);
+                    *reinterpret_cast<Piece<E, W> *>(to + ea) = a[k];
+                    *reinterpret_cast<Piece<E, W> *>(to + eb) = b[k];
                 }
                 to += dst_step;
                 --left;
@@ -215,6 +219,45 @@ __device__ __forceinline__ bool rope_walk(const RopeLane<W, HALF> &me, const E *
         }
     }
     return true;
+}
+
+// Copies `bytes` bytes of each of H heads (strides in bytes) by pieces of type P, every `shares`-th 32 pieces from
+// share `share` on.  ready() as in rope_walk.
+template <typename P, typename Ready, typename Dst>
+__device__ __forceinline__ bool copy_pieces(const uint8_t *src, int64_t src_head, int64_t dst_head, int H, int bytes,
+                                            int share, int shares, Ready ready, Dst dst)
+{
+    const int per_head = bytes / (int)sizeof(P), pieces = per_head * H, lane = threadIdx.x & 31;
+    for (int i0 = share * 32 + lane; i0 - lane < pieces; i0 += kRopeCopies * 32 * shares) {
+        P a[kRopeCopies];
+#pragma unroll
+        for (int k = 0; k < kRopeCopies; ++k) {
+            const int i = i0 + k * 32 * shares, h = i / per_head;
+            if (i < pieces) a[k] = *reinterpret_cast<const P *>(src + h * src_head + (i - h * per_head) * (int)sizeof(P));
+        }
+        if (!ready()) return false;
+        uint8_t *to = dst();
+#pragma unroll
+        for (int k = 0; k < kRopeCopies; ++k) {
+            const int i = i0 + k * 32 * shares, h = i / per_head;
+            if (i < pieces) *reinterpret_cast<P *>(to + h * dst_head + (i - h * per_head) * (int)sizeof(P)) = a[k];
+        }
+    }
+    return true;
+}
+
+// The same with pieces of `piece` bytes (16, 8, 4 or 2), which the host has found to fit.
+template <typename Ready, typename Dst>
+__device__ __forceinline__ bool copy_heads(int piece, const void *src, int64_t src_head, int64_t dst_head, int H, int bytes,
+                                           int share, int shares, Ready ready, Dst dst)
+{
+    const uint8_t *from = static_cast<const uint8_t *>(src);
+    switch (piece) {
+    case 16: return copy_pieces<uint4>(from, src_head, dst_head, H, bytes, share, shares, ready, dst);
+    case 8: return copy_pieces<uint2>(from, src_head, dst_head, H, bytes, share, shares, ready, dst);
+    case 4: return copy_pieces<uint32_t>(from, src_head, dst_head, H, bytes, share, shares, ready, dst);
+    default: return copy_pieces<uint16_t>(from, src_head, dst_head, H, bytes, share, shares, ready, dst);
+    }
 }
 
 struct RopeParams {
@@ -227,6 +270,7 @@ struct RopeParams {
     int32_t H, D, R;
     float scale;
     int32_t inverse;
+    int32_t copy_piece;  // bytes; 0: entries R .. D-1 are not copied (none, or y is x)
 };
 
 // `shares` warps take a token's heads in turn.
@@ -239,17 +283,23 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const R
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
-    const RopeLane<W, HALF> me(p.D, p.R);
+    const RopeLane<W> me(p.R);
+    const int share = (int)(gw - t * shares);
+    const E *x = static_cast<const E *>(p.x) + t * p.x_token;
+    E *y = static_cast<E *>(p.y) + t * p.y_token;
     bool have = false;
     rope_walk<E, W, HALF>(
-        me, static_cast<const E *>(p.x) + t * p.x_token, p.x_head, p.y_head, p.H, p.R, (int)(gw - t * shares), shares, cs,
-        p.x != p.y,
+        me, x, p.x_head, p.y_head, p.H, p.R, share, shares, cs,
         [&] {
-            if (!have && p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
+            if (!have) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
             have = true;
             return true;
         },
-        [&] { return static_cast<E *>(p.y) + t * p.y_token; });
+        [&] { return y; });
+    if (p.copy_piece)
+        copy_heads(
+            p.copy_piece, x + p.R, p.x_head * (int)sizeof(E), p.y_head * (int)sizeof(E), p.H, (p.D - p.R) * (int)sizeof(E),
+            share, shares, [] { return true; }, [&] { return reinterpret_cast<uint8_t *>(y + p.R); });
 }
 
 // ------------------------------------------------------------------------------- paged append
@@ -284,6 +334,7 @@ struct AppendParams {
     const double *inv_freq;    // null when R = 0
     int64_t T, pages;
     int32_t B, Hq, Hkv, D, R, page_size, max_pages;
+    int32_t rest_piece, v_piece;  // bytes per copied piece of entries R .. D-1 of queries and keys (0: none), and of values
     float scale;
     int32_t *status;
 };
@@ -328,7 +379,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
     griddep_launch_dependents();
     if (t >= p.T) return;
     const int share = (int)(gw - t * shares);
-    const RopeLane<W, HALF> me(p.D, p.R);
+    const RopeLane<W> me(p.R);
     AppendSlot slot{-1, 0};
     bool have = false;
     auto ready = [&] {
@@ -339,34 +390,29 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
         }
         return slot.cache >= 0;
     };
+    const E *q = p.q + t * p.q_token, *k = p.k + t * p.k_token, *v = p.v + t * p.v_token;
+    E *qo = p.q_out + t * p.qo_token;
+    auto bytes_at = [](E *e) { return reinterpret_cast<uint8_t *>(e); };
+    constexpr int kE = sizeof(E);
     int group = share;  // the warp's next group of heads; the key heads go on where the query heads end
     if (p.q != nullptr) {
-        if (!rope_walk<E, W, HALF>(me, p.q + t * p.q_token, p.q_head, p.qo_head, p.Hq, p.R, group, shares, cs, true, ready,
-                                   [&] { return p.q_out + t * p.qo_token; }))
-            return;
+        if (!rope_walk<E, W, HALF>(me, q, p.q_head, p.qo_head, p.Hq, p.R, group, shares, cs, ready, [&] { return qo; })) return;
         group = (share + shares - (p.Hq + me.heads - 1) / me.heads % shares) % shares;
     }
-    if (!rope_walk<E, W, HALF>(me, p.k + t * p.k_token, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, true, ready,
+    if (!rope_walk<E, W, HALF>(me, k, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, ready,
                                [&] { return p.k_cache + slot.cache; }))
         return;
-    // The values: pieces of all heads in a row.
-    const E *vv = p.v + t * p.v_token;
-    const int per_v = p.D / W, pieces = per_v * p.Hkv;
-    for (int i0 = share * 32 + lane; i0 - lane < pieces; i0 += kRopeCopies * 32 * shares) {
-        Piece<E, W> a[kRopeCopies];
-#pragma unroll
-        for (int k = 0; k < kRopeCopies; ++k) {
-            const int i = i0 + k * 32 * shares, h = i / per_v;
-            if (i < pieces) a[k] = *reinterpret_cast<const Piece<E, W> *>(vv + h * p.v_head + (i - h * per_v) * W);
-        }
-        if (!ready()) return;
-#pragma unroll
-        for (int k = 0; k < kRopeCopies; ++k) {
-            const int i = i0 + k * 32 * shares, h = i / per_v;
-            if (i < pieces)
-                *reinterpret_cast<Piece<E, W> *>(p.v_cache + slot.cache + h * p.c_head + (i - h * per_v) * W) = a[k];
-        }
+    if (p.rest_piece) {
+        const int rest = (p.D - p.R) * kE;
+        if (p.q != nullptr && !copy_heads(p.rest_piece, q + p.R, p.q_head * kE, p.qo_head * kE, p.Hq, rest, share, shares,
+                                          ready, [&] { return bytes_at(qo + p.R); }))
+            return;
+        if (!copy_heads(p.rest_piece, k + p.R, p.k_head * kE, p.c_head * kE, p.Hkv, rest, share, shares, ready,
+                        [&] { return bytes_at(p.k_cache + slot.cache + p.R); }))
+            return;
     }
+    copy_heads(p.v_piece, v, p.v_head * kE, p.c_head * kE, p.Hkv, p.D * kE, share, shares, ready,
+               [&] { return bytes_at(p.v_cache + slot.cache); });
 }
 
 }  // namespace bi
