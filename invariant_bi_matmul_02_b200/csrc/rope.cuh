@@ -46,12 +46,12 @@ struct alignas(2 * sizeof(E)) Piece<E, 2> {
 };
 
 // A lane's buffers: one head is turned while the others are on their way.  More for smaller pieces, as registers
-// allow (8284 tokens of 19 heads of 192: single bf16 entries 85 us with 4, 116 with 2; pairs of them 73 with 2, 108
-// with 4; pairs of fp32 entries 37 with 6, 46 with 2; 16-byte pieces of 8192 x 40 x 128 31.4 with 2, 32.5 with 3).
+// allow (8284 tokens of 19 heads of 192, 74 bf16 entries turned one by one: 57.7 us with 6, 88.8 with 2; 20 by
+// twos: 35.2 with 4, 37.8 with 2; 16-byte pieces of 8192 x 40 x 128: 31.4 with 2, 32.5 with 3).
 template <typename E, int W>
 __host__ __device__ constexpr int rope_buffers()
 {
-    return W == 1 ? 4 : W == 2 && sizeof(E) == 4 ? 6 : 2;
+    return W == 1 ? 6 : W == 2 ? 4 : 2;
 }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -372,7 +372,6 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
 {
     using E = __nv_bfloat16;
     extern __shared__ __align__(16) float rope_cs[];  // [kRopeWarps][R]
-    const int lane = threadIdx.x & 31;
     float *cs = rope_cs + (threadIdx.x >> 5) * p.R;
     const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
     griddep_wait();

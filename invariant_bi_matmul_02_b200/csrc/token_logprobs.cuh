@@ -227,39 +227,44 @@ __device__ __forceinline__ float tl_element(const void *row, int e)
     return static_cast<const float *>(row)[e];
 }
 
-constexpr int kTlColumns = 128;  // candidate threads, groups and elements the short way takes
+constexpr int kTlColumns = 128;  // candidate threads, groups and elements of the short way
 constexpr int kTlGroups = 128;
-constexpr int kTlKeys = 256;
+constexpr int kTlKeys = kTlMaxTop + kTlWarps * 32;
+constexpr int kTlCrowd = (kTlMaxTop - 1) * kTlMaxPieces;  // groups above the k-th thread's best, at most
 
 struct TlScratch {
     uint64_t keys[kTlKeys];
-    int32_t groups[kTlGroups];
+    uint16_t groups[kTlCrowd];  // numbers i: piece i / kTlThreads of the block, thread i % kTlThreads
+    uint16_t columns[kTlColumns];
     uint32_t range[2][kTlWarps];
-    int32_t columns[kTlColumns];
     int32_t n_columns, n_groups, n_keys;
 };
 
 // The block's `top` best keys, in order, to out[] (places without an element: 0).  tl_max holds its `local`
-// pieces' group maxima, one column per thread; `mine` is the ordered largest of
-// the thread's own (0: NaN or none).
+// pieces' group maxima, one column per thread; `mine` is the ordered largest of the thread's own (0: NaN or none).
 //   1. A bound that at least `top` groups reach: bisection over the ordered values of the threads' best
 //      groups, until few more than `top` threads reach it (or it is exact).
 //   2. The groups of those threads that reach it are listed, read again, and their elements
 //      that reach it listed: at least `top` elements do, so the best are among them.
 //   3. An element's place is the number of larger keys.
-// False when a list overflows: many equal values around the k-th.  All threads agree.
+// Where a list overflows (many equal values around the k-th, such as a mask's), the long way: with the bound
+// exact, fewer than `top` threads have a group above it.  The elements above the bound are read from those groups (more
+// than fit: each warp keeps a sorted list of its share), and one warp takes the first `top` elements that equal it, in
+// index order.
 template <bool BF16>
-__device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *row, int rank, int local,
+__device__ __forceinline__ void tl_best_groups(const TlParams &p, const void *row, int rank, int local,
                                                const float *tl_max, uint32_t mine, TlScratch &s, uint64_t *out)
 {
     constexpr int kGroup = tl_group(BF16), kPiece = tl_piece(BF16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto first = [&](int i) { return (i / kTlThreads * p.cluster + rank) * kPiece + kGroup * (i % kTlThreads); };
     const uint32_t top_of_warp = __reduce_max_sync(0xffffffffu, mine), low_of_warp = __reduce_min_sync(0xffffffffu, mine);
     if (lane == 0) {
         s.range[0][warp] = low_of_warp;
         s.range[1][warp] = top_of_warp;
     }
     for (int j = tid; j < kTlKeys; j += kTlThreads) s.keys[j] = 0;
+    if (tid < kTlMaxTop) out[tid] = 0;
     if (tid == 0) s.n_columns = s.n_groups = s.n_keys = 0;
     __syncthreads();
     // Invariant: at least `top` threads reach lo (or lo is the least of all: every group is a candidate), fewer reach hi.
@@ -270,62 +275,133 @@ __device__ __forceinline__ bool tl_best_groups(const TlParams &p, const void *ro
         hi = max(hi, s.range[1][w]);
     }
     ++hi;
-    const int enough = 2 * p.top + 8;
-    while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int n = __syncthreads_count(mine >= mid);
-        if (n >= p.top) lo = mid;
-        else hi = mid;
-        if (n >= p.top && n <= enough) break;
-    }
+    auto halve = [&](int enough) {
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            const int n = __syncthreads_count(mine >= mid);
+            if (n >= p.top) lo = mid;
+            else hi = mid;
+            if (n >= p.top && n <= enough) break;
+        }
+    };
+    halve(2 * p.top + 8);
     if (mine >= lo) {
         const int at = atomicAdd(&s.n_columns, 1);
-        if (at < kTlColumns) s.columns[at] = tid;
+        if (at < kTlColumns) s.columns[at] = (uint16_t)tid;
     }
     __syncthreads();
     const int n_columns = s.n_columns;
-    if (n_columns > kTlColumns) return false;
-    for (int j = tid; j < n_columns * local; j += kTlThreads) {
-        const int column = s.columns[j / local], piece = j % local;
-        const int e0 = (piece * p.cluster + rank) * kPiece + kGroup * column;
-        if (tl_order(tl_max[piece * kTlThreads + column]) >= lo && e0 < p.V) {
-            const int at = atomicAdd(&s.n_groups, 1);
-            if (at < kTlGroups) s.groups[at] = e0;
-        }
-    }
-    __syncthreads();
-    const int n_groups = s.n_groups;
-    if (n_groups > kTlGroups) return false;
-    constexpr int kBatch = 6;  // elements a thread has in flight
-    for (int i0 = tid; i0 - tid < n_groups * kGroup; i0 += kBatch * kTlThreads) {
-        float v[kBatch];
-        int e[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + k * kTlThreads;
-            e[k] = i < n_groups * kGroup ? s.groups[i / kGroup] + i % kGroup : p.V;
-            v[k] = e[k] < p.V ? tl_element<BF16>(row, e[k]) : 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (e[k] < p.V && tl_order(v[k]) >= lo) {
-                const int at = atomicAdd(&s.n_keys, 1);
-                if (at < kTlKeys) s.keys[at] = tl_key(v[k], (uint32_t)e[k]);
+    int n = kTlKeys + 1;  // keys listed; more than fit: the long way
+    if (n_columns <= kTlColumns) {
+        for (int j = tid; j < n_columns * local; j += kTlThreads) {
+            const int i = j % local * kTlThreads + s.columns[j / local];
+            if (tl_order(tl_max[i]) >= lo && first(i) < p.V) {
+                const int at = atomicAdd(&s.n_groups, 1);
+                if (at < kTlGroups) s.groups[at] = (uint16_t)i;
             }
-    }
-    if (tid < kTlMaxTop) out[tid] = 0;
-    __syncthreads();
-    const int n = s.n_keys;
-    if (n > kTlKeys) return false;
-    if (tid < n) {
-        const uint64_t key = s.keys[tid];
-        int place = 0;
-        for (int j = 0; j < n; j += 4)
+        }
+        __syncthreads();
+        const int n_groups = s.n_groups;
+        if (n_groups <= kTlGroups) {
+            constexpr int kBatch = 6;  // elements a thread has in flight
+            for (int i0 = tid; i0 - tid < n_groups * kGroup; i0 += kBatch * kTlThreads) {
+                float v[kBatch];
+                int e[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) place += s.keys[j + k] > key;  // 0 past the n-th
-        if (place < p.top) out[place] = key;
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * kTlThreads;
+                    e[k] = i < n_groups * kGroup ? first(s.groups[i / kGroup]) + i % kGroup : p.V;
+                    v[k] = e[k] < p.V ? tl_element<BF16>(row, e[k]) : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (e[k] < p.V && tl_order(v[k]) >= lo) {
+                        const int at = atomicAdd(&s.n_keys, 1);
+                        if (at < kTlKeys) s.keys[at] = tl_key(v[k], (uint32_t)e[k]);
+                    }
+            }
+            __syncthreads();
+            n = s.n_keys;
+        }
     }
-    return true;
+    if (n > kTlKeys) {
+        halve(0);
+        __syncthreads();
+        if (tid == 0) s.n_groups = 0;
+        __syncthreads();
+        if (mine > lo)
+            for (int i = tid; i < local * kTlThreads; i += kTlThreads)
+                if (first(i) < p.V && tl_order(tl_max[i]) > lo) s.groups[atomicAdd(&s.n_groups, 1)] = (uint16_t)i;
+        __syncthreads();
+        const int n_groups = s.n_groups;
+        constexpr int kBatch = 4;  // groups a warp has in flight
+        for (int j = tid; j < kTlKeys; j += kTlThreads) s.keys[j] = 0;
+        if (tid == 0) s.n_keys = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int more = p.top;
+            for (int i0 = 0; i0 < local * kTlThreads && more > 0; i0 += 32) {
+                const int i = i0 + lane;
+                unsigned reach = __ballot_sync(0xffffffffu, first(i) < p.V && tl_order(tl_max[i]) >= lo);
+                while (reach && more > 0) {
+                    uint32_t o[kBatch];
+                    int e[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        e[k] = reach && lane < kGroup ? first(i0 + __ffs(reach) - 1) + lane : p.V;
+                        o[k] = e[k] < p.V ? tl_order(tl_element<BF16>(row, e[k])) : 0u;
+                        reach &= reach - 1;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const unsigned same = __ballot_sync(0xffffffffu, e[k] < p.V && o[k] == lo);
+                        const int at = p.top - more + __popc(same & ((1u << lane) - 1));
+                        if ((same >> lane & 1u) && at < p.top) s.keys[at] = (uint64_t)lo << 32 | (uint32_t)~e[k];
+                        more -= __popc(same);
+                    }
+                }
+            }
+        } else {
+            // Above the bound: straight into the keys, as long as they fit.
+            for (int g = warp - 1; g < n_groups; g += kTlWarps - 1) {
+                const int e = lane < kGroup ? first(s.groups[g]) + lane : p.V;
+                const float v = e < p.V ? tl_element<BF16>(row, e) : 0.0f;
+                if (e < p.V && tl_order(v) > lo) {
+                    const int at = kTlMaxTop + atomicAdd(&s.n_keys, 1);
+                    if (at < kTlKeys) s.keys[at] = tl_key(v, (uint32_t)e);
+                }
+            }
+        }
+        __syncthreads();
+        if (s.n_keys > kTlKeys - kTlMaxTop) {
+            TlList list;
+            for (int g0 = warp; g0 < n_groups; g0 += kBatch * kTlWarps) {
+                float v[kBatch];
+                int e[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int g = g0 + k * kTlWarps;
+                    e[k] = g < n_groups && lane < kGroup ? first(s.groups[g]) + lane : p.V;
+                    v[k] = e[k] < p.V ? tl_element<BF16>(row, e[k]) : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    list.offer(e[k] < p.V && tl_order(v[k]) > lo ? tl_key(v[k], (uint32_t)e[k]) : 0, p.top);
+            }
+            s.keys[kTlMaxTop + tid] = list.mine;
+            __syncthreads();
+        }
+        n = kTlKeys;
+    }
+    for (int i = tid; i < n; i += kTlThreads) {
+        const uint64_t key = s.keys[i];
+        int place = 0;
+        if (key != 0)
+            for (int j = 0; j < n; j += 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) place += s.keys[j + k] > key;  // 0 past the n-th
+        if (key != 0 && place < p.top) out[place] = key;
+    }
 }
 
 // Grid M * cluster blocks of kTlThreads; block r of a row's cluster takes pieces r, r + cluster, ...
@@ -396,28 +472,8 @@ __global__ void __launch_bounds__(kTlThreads, kTlBlocks) token_logprobs_kernel(c
     }
     __syncthreads();
 
-    if (p.top > 0) {
-        const bool found = tl_best_groups<BF16>(p, row, rank, local, tl_max, tl_order(thread_best), scratch, bests[rank]);
-        if (!found && warp == 0) {
-            // Too many groups or elements tie near the k-th: warp 0 walks the maxima in index order and reads
-            // again only the groups that beat the k-th key so far.
-            TlList list;
-            for (int i0 = 0; i0 < local * kTlThreads; i0 += 32) {
-                const int i = i0 + lane;
-                const int e0 = ((i / kTlThreads) * p.cluster + rank) * kPiece + kGroup * (i % kTlThreads);
-                const uint64_t gk = e0 < p.V ? tl_key(tl_max[i], (uint32_t)e0) : 0;
-                unsigned better = __ballot_sync(0xffffffffu, gk > list.kth);
-                while (better) {
-                    const int src = __ffs(better) - 1;
-                    const int e = __shfl_sync(0xffffffffu, e0, src) + lane;
-                    list.offer(lane < kGroup && e < p.V ? tl_key(tl_element<BF16>(row, e), (uint32_t)e) : 0, p.top);
-                    better &= better - 1;
-                    better &= __ballot_sync(0xffffffffu, gk > list.kth);
-                }
-            }
-            bests[rank][lane] = list.mine;
-        }
-    }
+    if (p.top > 0)
+        tl_best_groups<BF16>(p, row, rank, local, tl_max, tl_order(thread_best), scratch, bests[rank]);
     if (p.cluster > 1) {
         cluster_sync_all();
         if (rank != 0) return;
