@@ -1144,6 +1144,11 @@ bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_pa
         rest = t;
     }
     p.box = (int32_t)box;
+    while ((1 << p.box_log2) < box) ++p.box_log2;
+    p.boxes = bi::kPgTile / (int32_t)box;
+    p.chunk = 32 / p.boxes;
+    p.by_page = bi::PgDivisor::of((uint32_t)cache->page_size);
+    p.by_heads = bi::PgDivisor::of((uint32_t)Hkv);
     p.heads_inner = cache->heads > 1 && (cache->page_size == 1 || cache->head_stride <= cache->token_stride) ? 1 : 0;
     CUtensorMap tm_k, tm_v;
     st = encode_page_map(&tm_k, cache->k, *cache, p.heads_inner != 0, (uint32_t)box);
@@ -1158,7 +1163,6 @@ bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_pa
     p.Hkv = (int32_t)Hkv;
     p.G = (int32_t)G;
     p.S = (int32_t)S;
-    p.page_size = (int32_t)cache->page_size;
     p.pages = (int32_t)cache->pages;
     p.max_len = (int32_t)max_len;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074);

@@ -60,6 +60,19 @@ struct PgShape {
     static constexpr int kSmem = kStages * kStageBytes + 2 * kOFloats * 4 + 1024;  // + alignment slack
 };
 
+// Quotients of numbers below 2^31 by a divisor that the host knows: n / d = n * mul >> shift, with
+// mul = ceil(2^shift / d) and shift = 31 + ceil(log2 d).
+struct PgDivisor {
+    uint32_t mul, shift, d;
+    __host__ static PgDivisor of(uint32_t d)
+    {
+        uint32_t l = 0;
+        while ((uint64_t(1) << l) < d) ++l;
+        return {(uint32_t)(((uint64_t(1) << (31 + l)) + d - 1) / d), 31 + l, d};
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (uint32_t)((uint64_t)n * mul >> shift); }
+};
+
 struct PgParams {
     const __nv_bfloat16 *q;
     int64_t q_row;  // entries between sequences
@@ -69,8 +82,11 @@ struct PgParams {
     float *part_o;     // [B, Hq, S, D]
     float2 *part_ml;   // [B, Hq, S] (maximum in units of log2, sum)
     __nv_bfloat16 *out;  // [B, Hq, D]
-    int32_t B, Hq, Hkv, G, S, page_size, pages, max_len;
+    int32_t B, Hq, Hkv, G, S, pages, max_len;
+    PgDivisor by_page, by_heads;  // page_size and Hkv
     int32_t box;          // tokens per TMA box: gcd(page_size, kPgTile)
+    int32_t box_log2, boxes;  // boxes per tile: kPgTile / box
+    int32_t chunk;        // tiles per 32 boxes
     int32_t heads_inner;  // dimension order of the tensor maps: (entry, head, token, page) or (entry, token, head, page)
     float scale_log2;     // score scale times log2(e)
     int32_t *status;
@@ -125,6 +141,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         abort_flag_s = 0;
         fence_mbar_init();
+    } else if (tid == 32 * kPgWarps) {
+        prefetch_tensor_map(&tm_k);
+        prefetch_tensor_map(&tm_v);
     }
     griddep_wait();  // the previous kernel's output (q, cache, lengths, table) is complete
     griddep_launch_dependents();
@@ -148,8 +167,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         if (lane == 31) warp_total[warp] = inc;
         __syncthreads();
-        int at = inc - sum;
-        for (int w = 0; w < warp; ++w) at += warp_total[w];
+        int at = inc - sum + (int)__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)warp_total[lane] : 0u);
         for (int j = 0; j < per && b0 + j < p.B; ++j) {
             first[b0 + j] = at;
             const int n = (int)pg_splits(lens_s[b0 + j]);
@@ -168,7 +186,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     // Items come in ascending order: the sequence is searched from the last one on, 32 at a time.
     int b = 0, first_b = 0;
     auto item = [&](uint32_t it) -> Item {
-        const int sg = (int)(it / n_kv), g = (int)(it - (uint32_t)sg * n_kv);
+        const int sg = (int)p.by_heads.quotient(it), g = (int)(it - (uint32_t)sg * n_kv);
         int passed;
         do {
             const int v = b + 1 + lane < p.B ? first[b + 1 + lane] : 0x7fffffff;
@@ -188,8 +206,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // are issued by one warp in order, and its parity waits are exact.
         const uint32_t pw = (uint32_t)(warp - kPgWarps);
         const uint64_t policy = l2_policy_evict_first();  // every cache byte is read once
-        const int nb = kPgTile / p.box;                   // boxes per tile
-        const int chunk_tiles = 32 / nb;                  // tiles of a chunk: 32 boxes, one per lane
+        const int nb = p.boxes, chunk_tiles = p.chunk;    // a chunk is 32 boxes, one per lane
         // A chunk of an item: its lane's box, the page it lies in and its first row there.
         struct Chunk {
             Item w;
@@ -201,9 +218,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const int k = c.tile0 * kPgTile + lane * p.box;  // token within the item
             c.page = c.row = 0;
             if (k < c.w.n) {
-                const uint32_t t = (uint32_t)(c.w.t0 + k), at = t / (uint32_t)p.page_size;
+                const uint32_t t = (uint32_t)(c.w.t0 + k), at = p.by_page.quotient(t);
                 c.page = p.table[c.w.b * p.table_row + at];
-                c.row = (int32_t)(t - at * (uint32_t)p.page_size);
+                c.row = (int32_t)(t - at * p.by_page.d);
             }
         };
         auto enter = [&](Chunk &c, uint32_t it) {  // the first chunk of the next item with tokens, from item `it` on
@@ -219,22 +236,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         Chunk cur;
         enter(cur, blockIdx.x);
         while (ok && cur.it < items) {
-            // The next chunk's pages are looked up while this one's boxes are issued.
             const int tiles = (cur.w.n + kPgTile - 1) / kPgTile, end = cur.tile0 + chunk_tiles;
             Chunk next = cur;
-            if (end < tiles) {
-                next.tile0 = end;
-                look_up(next);
-            } else {
-                enter(next, cur.it + gridDim.x);
-            }
-            const int boxes = (cur.w.n + p.box - 1) / p.box;
+            auto look_ahead = [&] {
+                if (end < tiles) {
+                    next.tile0 = end;
+                    look_up(next);
+                } else {
+                    enter(next, cur.it + gridDim.x);
+                }
+            };
+            // The next chunk's pages are looked up while this one's boxes are issued (the first chunk's boxes go
+            // first).
+            const bool start = mine == 0 && cur.it == blockIdx.x;
+            if (!start) look_ahead();
             const uint32_t n0 = base + (uint32_t)cur.tile0;
             for (int j = cur.tile0 + (int)((pw - n0) % kPgProducers); j < end && j < tiles; j += kPgProducers) {
                 const uint32_t num = base + (uint32_t)j, stage = num % C::kStages, use = num / C::kStages;
                 ok = __all_sync(0xffffffffu, wait_bounded(&empty[stage], (use & 1u) ^ 1u, abort_flag, p.status, lim));
                 if (!ok) break;
-                const int k0 = j * nb, cnt = boxes - k0 < nb ? boxes - k0 : nb;
+                const int left = cur.w.n - kPgTile * j, cnt = left >= kPgTile ? nb : (left + p.box - 1) >> p.box_log2;
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(cnt * p.box * D * 2 * 2));
                 __syncwarp();
                 const int x = lane - (j - cur.tile0) * nb;
@@ -255,6 +276,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
                 ++mine;
             }
+            if (start) look_ahead();
             if (next.it != cur.it) base += (uint32_t)tiles;
             cur = next;
         }
