@@ -564,10 +564,12 @@ __global__ void __launch_bounds__(kPgCombineThreads)
                                    int max_len, int rows)
 {
     constexpr int kLanes = D / 4;
+    const int bh = (int)((blockIdx.x * (unsigned)kPgCombineThreads + threadIdx.x) / kLanes), c = threadIdx.x % kLanes;
+    // Launch 1 lets this kernel start once all its blocks have seen the inputs complete, so the lengths, which it
+    // does not write, need no wait.
+    const int n = bh < rows ? (int)pg_splits(pg_len(lens[bh / Hq], max_len)) : 0;
     griddep_wait();
     griddep_launch_dependents();
-    const int bh = (int)((blockIdx.x * (unsigned)kPgCombineThreads + threadIdx.x) / kLanes), c = threadIdx.x % kLanes;
-    const int n = bh < rows ? (int)pg_splits(pg_len(lens[bh / Hq], max_len)) : 0;
     const float2 *ml = part_ml + (int64_t)bh * S;
     float m = kNegInf;
     for (int s = c; s < n; s += kLanes) m = fmaxf(m, ml[s].x);
@@ -589,11 +591,11 @@ __global__ void __launch_bounds__(kPgCombineThreads)
     constexpr int kWarps = kPgCombineThreads / 32;
     __shared__ float red[kWarps], sl[kWarps];
     __shared__ float4 so[kWarps][8];
-    griddep_wait();
-    griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid / 8, c = tid % 8 + 8 * blockIdx.x;
     const int h = blockIdx.y, b = blockIdx.z;
-    const int n = (int)pg_splits(pg_len(lens[b], max_len));
+    const int n = (int)pg_splits(pg_len(lens[b], max_len));  // complete, as above
+    griddep_wait();
+    griddep_launch_dependents();
     if (n <= 1) return;  // written by launch 1
     const int64_t bh = (int64_t)b * Hq + h;
     const float2 *ml = part_ml + bh * S;

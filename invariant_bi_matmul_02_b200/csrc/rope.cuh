@@ -339,31 +339,27 @@ struct AppendParams {
     int32_t *status;
 };
 
-// Where one new token goes.
-struct AppendSlot {
-    int64_t cache;  // offset of its row in the cache (head 0), or -1: the token is skipped
-    int32_t pos;    // position that turns it
+// The place in its sequence that new token t takes, by a warp.
+struct AppendPlace {
+    int64_t at;       // place in the sequence
+    int32_t b;        // sequence, or -1: the token is skipped
+    int32_t page;     // what the table says, -1 where it says nothing
 };
 
-// One warp works out token t's slot.
-__device__ __forceinline__ AppendSlot append_slot(const AppendParams &p, int64_t t)
+__device__ __forceinline__ AppendPlace append_place(const AppendParams &p, int64_t t)
 {
     int b = (int)t, left = 1;  // tokens of the sequence from t on
     if (p.cu != nullptr) {
         b = warp_count_le(p.cu, p.B + 1, (int)t) - 1;
-        if (b < 0 || b >= p.B) return {-1, 0};  // before the first sequence or behind the last: not ours
+        if (b < 0 || b >= p.B) return {0, -1, -1};  // before the first sequence or behind the last: not ours
         left = p.cu[b + 1] - (int)t;
     }
     const int32_t len = p.lens[b];
-    if (len == 0) return {-1, 0};  // an empty place of a padded batch
+    if (len == 0) return {0, -1, -1};  // an empty place of a padded batch
     const int64_t at = (int64_t)len - left;
     int32_t page = -1;
     if (left >= 1 && at >= 0 && at / p.page_size < p.max_pages) page = p.table[b * p.table_row + at / p.page_size];
-    if (page < 0 || page >= p.pages) {
-        *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
-        return {-1, 0};
-    }
-    return {page * p.c_page + (at % p.page_size) * p.c_token, p.positions ? p.positions[t] : (int32_t)at};
+    return {at, b, page};
 }
 
 // `shares` warps take a token's query heads, key heads and values in turn.
@@ -379,15 +375,21 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
     if (t >= p.T) return;
     const int share = (int)(gw - t * shares);
     const RopeLane<W> me(p.R);
-    AppendSlot slot{-1, 0};
+    int64_t row = -1;  // offset of the token's row in the cache (head 0), or -1: the token is skipped
     bool have = false;
     auto ready = [&] {
         if (!have) {
-            slot = append_slot(p, t);
-            if (slot.cache >= 0 && p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, slot.pos, p.scale, false);
+            const AppendPlace w = append_place(p, t);
             have = true;
+            if (w.b < 0) return false;
+            // The angles do not need the page, which is still on its way.
+            if (p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, p.positions ? p.positions[t] : (int32_t)w.at, p.scale, false);
+            if (w.page < 0 || w.page >= p.pages)
+                *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+            else
+                row = w.page * p.c_page + (w.at % p.page_size) * p.c_token;
         }
-        return slot.cache >= 0;
+        return row >= 0;
     };
     const E *q = p.q + t * p.q_token, *k = p.k + t * p.k_token, *v = p.v + t * p.v_token;
     E *qo = p.q_out + t * p.qo_token;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
         group = (share + shares - (p.Hq + me.heads - 1) / me.heads % shares) % shares;
     }
     if (!rope_walk<E, W, HALF>(me, k, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, ready,
-                               [&] { return p.k_cache + slot.cache; }))
+                               [&] { return p.k_cache + row; }))
         return;
     if (p.rest_piece) {
         const int rest = (p.D - p.R) * kE;
@@ -407,11 +409,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
                                           ready, [&] { return bytes_at(qo + p.R); }))
             return;
         if (!copy_heads(p.rest_piece, k + p.R, p.k_head * kE, p.c_head * kE, p.Hkv, rest, share, shares, ready,
-                        [&] { return bytes_at(p.k_cache + slot.cache + p.R); }))
+                        [&] { return bytes_at(p.k_cache + row + p.R); }))
             return;
     }
     copy_heads(p.v_piece, v, p.v_head * kE, p.c_head * kE, p.Hkv, p.D * kE, share, shares, ready,
-               [&] { return bytes_at(p.v_cache + slot.cache); });
+               [&] { return bytes_at(p.v_cache + row); });
 }
 
 }  // namespace bi
