@@ -76,7 +76,7 @@ bi_status paged_smem_opt_in()
 }
 
 // Shared memory of a token_logprobs block that takes `pieces` pieces.
-inline size_t token_logprobs_smem(int64_t pieces, int64_t top) { return top > 0 ? (size_t)pieces * bi::kTlThreads * 4 : 0; }
+inline size_t token_logprobs_smem(int64_t pieces, int64_t top) { return top > 0 ? (size_t)pieces * bi::kTlThreads * sizeof(uint16_t) : 0; }
 
 bi_status token_logprobs_smem_opt_in()
 {
