@@ -493,7 +493,7 @@ def bi_paged_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     """One decode step over a paged cache: q [B, Hq, D] (rows may be strided), caches [pages, page_size, heads, D],
     block_table [B, max_pages] and seq_lens [B] int32.  max_len: the longest sequence as the host knows it (default:
     all the table can name; a tighter bound needs less scratch).  scratch: device memory of at least
-    bi_paged_decode_attention_scratch_bytes, allocated when None (not on a stream other than the current one)."""
+    bi_paged_decode_attention_scratch_bytes, allocated when None."""
     return (_marshal or load_marshal()).paged_decode_attention(
         q, k_cache, v_cache, block_table, seq_lens, max_len, scale, scratch, out,
         stream if stream is None else _stream(stream))

@@ -1117,6 +1117,7 @@ bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_pa
     bi_status st = check_cache(cache);
     if (st != BI_OK) return st;
     const int64_t D = cache->head_dim, Hkv = cache->heads;
+    if (B == 0) return BI_OK;
     if (B < 0 || Hq <= 0 || max_len <= 0 || max_pages <= 0 || Hq % Hkv != 0) return BI_ERR_INVALID_ARG;
     const int64_t G = Hq / Hkv;
     if ((D != 64 && D != 128) || G > 16) return BI_ERR_UNSUPPORTED;
@@ -1124,7 +1125,6 @@ bi_status bi_paged_decode_attention(const void *q, int64_t q_stride, const bi_pa
     if (max_len > max_pages * cache->page_size) return BI_ERR_INVALID_ARG;
     const int64_t S = bi::pg_splits(max_len), Bl = B < bi::kPgSeqs ? B : bi::kPgSeqs;
     if (Bl * S > kI32Max || Bl * S * Hkv > kI32Max) return BI_ERR_UNSUPPORTED;  // item numbers are 32-bit
-    if (B == 0) return BI_OK;
     if (!q || !block_table || !seq_lens || !out || (S > 1 && !scratch)) return BI_ERR_INVALID_ARG;
     if ((B > 1 && (q_stride < Hq * D || table_stride < max_pages))) return BI_ERR_INVALID_ARG;
     if (scratch_bytes < bi_paged_decode_attention_scratch_bytes(B, Hq, D, max_len)) return BI_ERR_INVALID_ARG;

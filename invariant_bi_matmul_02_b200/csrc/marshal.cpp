@@ -10,11 +10,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <string>
 
@@ -289,10 +291,11 @@ PyObject *paged_decode_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (!scratch->is_contiguous()) value_error("scratch must be contiguous");
     }
     void *s = stream_of(a[9], dev);
-    // Scratch made here is freed when this returns, on torch's current stream; a call on another stream
-    // must not find it reused while it still runs.
-    if (own.defined() && a[9] != Py_None && s != c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream())
-        value_error("on a stream other than the current one, pass scratch");
+    // Scratch made here is freed when this returns, for reuse on torch's current stream: work on another stream
+    // is made known to the allocator.
+    if (own.defined() && a[9] != Py_None)
+        c10::cuda::CUDACachingAllocator::recordStream(
+            own.storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), (c10::DeviceIndex)dev));
     BI_CALL("bi_paged_decode_attention", p_paged_decode_attention, ptr(q), q.stride(0), &cache,
             static_cast<const int32_t *>(ptr(table)), table_stride, max_pages, static_cast<const int32_t *>(ptr(lens)),
             ptr(o), B, Hq, max_len, scale, ptr(*scratch), scratch->nbytes(), s)

@@ -93,7 +93,7 @@ def test_paged_attention_refusals(lib):
     for bad in (dict(q=FAKE + 2), dict(out=FAKE + 8), dict(lens=FAKE + 2), dict(table=FAKE + 1), dict(qs=1028),
                 dict(mp=100, ts=100, max_len=600, scratch=FAKE + 4)):
         assert attend(**bad) == A, bad
-    assert attend(B=0, q=NULL) == OK
+    assert attend(B=0, q=NULL) == OK and attend(B=0, mp=0, max_len=0) == OK
     need = lib.bi_paged_decode_attention_scratch_bytes
     assert need(4, 8, 128, 512) == 0 and need(0, 8, 128, 999) == 0
     assert need(4, 8, 128, 513) == 4 * 8 * 3 * (128 * 4 + 8)

@@ -164,6 +164,25 @@ def test_attention_more_sequences_than_one_launch_takes():
         assert same_bits(bi.bi_paged_decode_attention(q[i:i + 1], kc, vc, table[i:i + 1], sl[i:i + 1], max_len=int(sl[i])), o[i:i + 1])
 
 
+@pytest.mark.parametrize("page,Hkv", [(1, 1), (64, 1), (64, 3), (1, 2), (7, 1)])
+def test_one_page_caches(page, Hkv):
+    """A cache of one page, and pages or heads of one entry: strides that are never stepped over may be anything."""
+    g = gen(page + Hkv)
+    kc, vc = make_cache(g, 1, page, Hkv, 64)
+    odd = [1 if n == 1 else s for n, s in zip(kc.shape, kc.stride())]
+    kc, vc = kc.as_strided(kc.shape, odd), vc.as_strided(vc.shape, odd)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    sl = torch.tensor([page], dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(1, Hkv, 64, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(1, 2 * Hkv, 64, generator=g, device=DEV).to(torch.bfloat16)
+    bi.bi_paged_append(k, v, kc, vc, table, sl)
+    assert same_bits(kc[0, -1], k[0]) and same_bits(vc[0, -1], v[0])
+    close(bi.bi_paged_decode_attention(q, kc, vc, table, sl), *attend_definition(q, kc, vc, table, [page], 0.125))
+    empty = bi.bi_paged_decode_attention(q[:0], kc, vc, table[:0, :0], sl[:0])
+    assert empty.shape == (0, 2 * Hkv, 64)
+    assert bi.bi_get_device_status() == bi.BI_OK
+
+
 def test_attention_offsets_beyond_32_bits():
     """A cache of more than 2^32 elements: pages at its far end are read and written where they are."""
     page, Hkv, D = 64, 8, 128
@@ -242,6 +261,12 @@ def test_attention_streams_graphs_and_scratch():
     assert same_bits(out, want) and bool((scratch[need:] == 0xFF).all())
     with pytest.raises(bi.BiError):
         bi.bi_paged_decode_attention(q, kc, vc, table, sl, scratch=scratch[:need - 16])
+    # On another stream without scratch: the allocation made for the call outlives its work there.
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    made = [bi.bi_paged_decode_attention(q, kc, vc, table, sl, stream=side) for _ in range(20)]
+    side.synchronize()
+    assert all(same_bits(o, want) for o in made)
     # Two calls at once on two streams, each with its own scratch.
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
