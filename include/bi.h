@@ -27,6 +27,9 @@
  *     block size and each thread's element set depend only on the row length;
  *     partial results merge through a fixed warp-shuffle tree and a fixed
  *     cross-warp tree.
+ *   - bi_paged_decode_attention / bi_token_logprobs: cuts fixed by the sequence's own length
+ *     or the row's; how many blocks share the pieces may follow the batch, their order of folding
+ *     does not.
  *
  * Conventions shared by every entry point
  *   - Tensors are row-major.  Pointers marked "device" point to global memory
@@ -39,13 +42,13 @@
  *     call's own launches: an error left by another library's earlier launch on the thread
  *     is neither reported nor cleared (apart from a context-wide fault, which fails every
  *     launch).  The GEMM, RMSNorm, mean,
- *     one-block log_softmax and decode-attention kernels are launched with programmatic
- *     stream serialization:
+ *     one-block log_softmax, decode-attention (dense and paged), rotation, append and token
+ *     log-probability kernels are launched with programmatic stream serialization:
  *     they may start their on-chip set-up while the previous kernel on the stream drains,
  *     and read or write global memory only after that kernel has completed, so stream
  *     order holds as for any launch.
  *   - M = 0 (no rows) is a no-op that returns BI_OK.
- *   - Outputs must not overlap inputs.
+ *   - Outputs must not overlap inputs, except where an entry point allows an input as its output.
  *   - bf16 is IEEE-style bfloat16 (1-8-7); every bf16 output is rounded once,
  *     to nearest-even, from an fp32 value.
  *   - The library keeps per-device state for the life of the process (the SM count, the

@@ -3,8 +3,9 @@
 //
 // The library allocates no device memory.  Per device it caches the SM count, the
 // address of its status word and the GEMM kernel's shared-memory attribute.  No
-// launch decision depends on M except the grid size (how many CTAs share the tile
-// list, or how many rows there are), which never changes a row's arithmetic.
+// launch decision depends on M except how the work is shared (how many CTAs walk the tile
+// list, how many rows there are, how many blocks or warps take a row's or a token's
+// pieces), which never changes a row's arithmetic.
 #include "bi.h"
 
 #include <cuda.h>
