@@ -378,7 +378,8 @@ typedef struct {
  * Tokens behind cu_new[B] (or before cu_new[0]) and those of a sequence with seq_lens[b] = 0 are skipped:
  * nothing of theirs is read back or written.  A place that is negative or past the table, or a page
  * outside 0 .. pages-1, records BI_ERR_INVALID_ARG in the device status word and skips the token.
- * Two tokens must not share a place: pages that receive tokens belong to one sequence.
+ * Two tokens must not share a place: pages that receive tokens belong to one sequence.  (Where two do, each
+ * entry there is one of theirs, which one is not defined.)
  * D <= 1024, heads and Hq <= 65535, T, B < 2^31, pages and page_size <= 2^31 - 1.
  * Pieces as in bi_rope; k, v, q need no alignment beyond their type's.
  */
