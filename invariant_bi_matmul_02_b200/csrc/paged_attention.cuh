@@ -511,7 +511,22 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // the sequence's own number of splits, so both kernels below give a sequence the same bits.
 constexpr int kPgCombineThreads = 256;
 constexpr int kPgSerial = 32;
-constexpr int kPgAhead = 8;  // splits whose values a thread has in flight
+constexpr int kPgAhead = 16;  // splits whose values a thread has in flight
+
+// Splits s0, s0 + step, ... below n (at most kPgAhead): four columns of each and its maximum and sum.
+struct PgBatch {
+    float4 x[kPgAhead];
+    float2 w[kPgAhead];
+    __device__ __forceinline__ void load(const float2 *ml, const float4 *v, int row, int s0, int step, int n)
+    {
+#pragma unroll
+        for (int k = 0; k < kPgAhead; ++k) {
+            const int s = s0 + k * step;
+            x[k] = s < n ? v[(int64_t)s * row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
+        }
+    }
+};
 
 struct PgFold {
     float l = 0.0f;
@@ -525,20 +540,16 @@ struct PgFold {
         o.z = __fmaf_rn(v.z, f, o.z);
         o.w = __fmaf_rn(v.w, f, o.w);
     }
-    // Splits first, first + step, ... below n; lanes of a row hold four columns each.
-    __device__ __forceinline__ void run(const float2 *ml, const float4 *v, int row, int first, int step, int n, float ref)
+    // Splits first, first + step, ... below n in order; `batch` holds the first of them.
+    __device__ __forceinline__ void run(PgBatch &batch, const float2 *ml, const float4 *v, int row, int first, int step, int n,
+                                        float ref)
     {
-        for (int s0 = first; s0 < n; s0 += kPgAhead * step) {
-            float4 x[kPgAhead];
-            float2 w[kPgAhead];
+        for (int s0 = first;;) {
 #pragma unroll
-            for (int k = 0; k < kPgAhead; ++k) {
-                const int s = s0 + k * step;
-                x[k] = s < n ? v[(int64_t)s * row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                w[k] = s < n ? ml[s] : make_float2(kNegInf, 0.0f);
-            }
-#pragma unroll
-            for (int k = 0; k < kPgAhead; ++k) add(x[k], w[k], ref);
+            for (int k = 0; k < kPgAhead; ++k) add(batch.x[k], batch.w[k], ref);
+            s0 += kPgAhead * step;
+            if (s0 >= n) break;
+            batch.load(ml, v, row, s0, step, n);
         }
     }
     __device__ __forceinline__ void store(__nv_bfloat16 *out) const
@@ -572,13 +583,16 @@ __global__ void __launch_bounds__(kPgCombineThreads)
     griddep_wait();
     griddep_launch_dependents();
     const float2 *ml = part_ml + (int64_t)bh * S;
+    const float4 *po = reinterpret_cast<const float4 *>(part_o + (int64_t)bh * S * D) + c;
+    PgBatch batch;  // on its way while the maximum (exact in any order) is found
+    if (n > 1) batch.load(ml, po, kLanes, 0, 1, n);
     float m = kNegInf;
     for (int s = c; s < n; s += kLanes) m = fmaxf(m, ml[s].x);
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (n <= 1) return;  // written by launch 1, or no such row
     PgFold f;
-    f.run(ml, reinterpret_cast<const float4 *>(part_o + (int64_t)bh * S * D) + c, kLanes, 0, 1, n, m == kNegInf ? 0.0f : m);
+    f.run(batch, ml, po, kLanes, 0, 1, n, m == kNegInf ? 0.0f : m);
     f.store(out + (int64_t)bh * D + 4 * c);
 }
 
@@ -601,6 +615,10 @@ __global__ void __launch_bounds__(kPgCombineThreads)
     const int64_t bh = (int64_t)b * Hq + h;
     const float2 *ml = part_ml + bh * S;
     const float4 *po = reinterpret_cast<const float4 *>(part_o + bh * S * D) + c;
+    const bool serial = n <= kPgSerial;
+    const int start = serial ? (grp == 0 ? 0 : n) : grp, step = serial ? 1 : kPgCombineThreads / 8;
+    PgBatch batch;
+    batch.load(ml, po, D / 4, start, step, n);
     float m = kNegInf;
     for (int s = tid; s < n; s += kPgCombineThreads) m = fmaxf(m, ml[s].x);
     m = pg_warp_max(m);
@@ -611,14 +629,11 @@ __global__ void __launch_bounds__(kPgCombineThreads)
     for (int k = 1; k < kWarps; ++k) m = fmaxf(m, red[k]);
     const float ref = m == kNegInf ? 0.0f : m;
     PgFold f;
-    if (n <= kPgSerial) {
-        if (grp == 0) {
-            f.run(ml, po, D / 4, 0, 1, n, ref);
-            f.store(out + bh * D + 4 * c);
-        }
+    f.run(batch, ml, po, D / 4, start, step, n, ref);
+    if (serial) {
+        if (grp == 0) f.store(out + bh * D + 4 * c);
         return;
     }
-    f.run(ml, po, D / 4, grp, kPgCombineThreads / 8, n, ref);
 #pragma unroll
     for (int o = 8; o < 32; o <<= 1) {
         f.l = __fadd_rn(f.l, __shfl_xor_sync(0xffffffffu, f.l, o));
