@@ -297,7 +297,7 @@ __device__ __forceinline__ void tl_best_groups(const TlParams &p, const void *ro
             if (n >= p.top && n <= enough) break;
         }
     };
-    halve(2 * p.top + 8);
+    halve(p.top + p.top / 2 + 6);
     if (mine >= lo) {
         const int at = atomicAdd(&s.n_columns, 1);
         if (at < kTlColumns) s.columns[at] = (uint16_t)tid;
