@@ -475,19 +475,27 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 consumers_sync(1 + grp);
                 for (int i = ct; i < heads * (D / 4); i += 32 * kPgGroupWarps) {
                     const int h = i / (D / 4), d = 4 * (i % (D / 4));
-                    float mx = gm[0][h];
-                    for (int t = 1; t < warps; ++t) mx = fmaxf(mx, gm[t][h]);
+                    // All loads at once; a warp without a tile counts with a maximum of -inf and zeros.
+                    float mt[kPgGroupWarps], lt[kPgGroupWarps], mx = kNegInf, sum = 0.0f;
+                    float4 v[kPgGroupWarps], r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int t = 0; t < kPgGroupWarps; ++t) {
+                        const bool some = t < warps;
+                        mt[t] = some ? gm[t][h] : kNegInf;
+                        lt[t] = some ? gl[t][h] : 0.0f;
+                        v[t] = some ? *reinterpret_cast<const float4 *>(so_grp + (t * 8 + h) * C::kORow + d) : r;
+                    }
+#pragma unroll
+                    for (int t = 0; t < kPgGroupWarps; ++t) mx = fmaxf(mx, mt[t]);
                     const float ref = mx == kNegInf ? 0.0f : mx;
-                    float sum = 0.0f;
-                    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int t = 0; t < warps; ++t) {
-                        const float f = ex2(gm[t][h] - ref);
-                        const float4 v = *reinterpret_cast<const float4 *>(so_grp + (t * 8 + h) * C::kORow + d);
-                        sum = __fmaf_rn(gl[t][h], f, sum);
-                        r.x = __fmaf_rn(v.x, f, r.x);
-                        r.y = __fmaf_rn(v.y, f, r.y);
-                        r.z = __fmaf_rn(v.z, f, r.z);
-                        r.w = __fmaf_rn(v.w, f, r.w);
+#pragma unroll
+                    for (int t = 0; t < kPgGroupWarps; ++t) {
+                        const float f = ex2(mt[t] - ref);
+                        sum = __fmaf_rn(lt[t], f, sum);
+                        r.x = __fmaf_rn(v[t].x, f, r.x);
+                        r.y = __fmaf_rn(v[t].y, f, r.y);
+                        r.z = __fmaf_rn(v[t].z, f, r.z);
+                        r.w = __fmaf_rn(v[t].w, f, r.w);
                     }
                     const int64_t bh = (int64_t)w.b * p.Hq + head0 + 8 * nt + h;
                     if (last) {
