@@ -474,6 +474,25 @@ __device__ __forceinline__ void load_32(const void *p, uint32_t *w)
                  : "l"(p));
 }
 
+// The two bf16 halves of a word, each less c in fp32 (a mixed-precision subtraction of sm_100a: nothing to widen first).
+__device__ __forceinline__ void sub_bf16x2(uint32_t w, float c, float &lo, float &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "sub.f32.bf16 %0, l, %3;\n\t"
+        "sub.f32.bf16 %1, h, %3;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(w), "f"(c));
+}
+
+// The largest value of the warp's lanes in one instruction; NaN counts as nothing.
+__device__ __forceinline__ float warp_max(float v)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
 // 2^x, to 2 units of the last place; results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x)
 {

@@ -172,10 +172,12 @@ struct TlGroup {
         w[4 * i + 2] = v.z;
         w[4 * i + 3] = v.w;
     }
-    __device__ __forceinline__ float2 pair(int i) const  // elements 2 i and 2 i + 1
+    __device__ __forceinline__ uint64_t less(int i, float ref) const  // elements 2 i and 2 i + 1, less ref
     {
-        if (BF16) return make_float2(bf16lo(w[i]), bf16hi(w[i]));
-        return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        if (!BF16) return f2_add(f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), f2_pack(-ref, -ref));
+        float lo, hi;
+        sub_bf16x2(w[i], ref, lo, hi);
+        return f2_pack(lo, hi);
     }
     __device__ __forceinline__ float max() const
     {
@@ -195,12 +197,11 @@ struct TlGroup {
     template <bool CLAMP>
     __device__ __forceinline__ void sums(float ref, float c, float &s, float &t) const
     {
-        const uint64_t neg = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
+        const uint64_t c2 = f2_pack(c, c);
         uint64_t s2 = 0, t2 = 0;
 #pragma unroll
         for (int i = 0; i < kSize / 2; ++i) {
-            const float2 v = pair(i);
-            uint64_t d2 = f2_mul(f2_add(f2_pack(v.x, v.y), neg), c2);
+            uint64_t d2 = f2_mul(less(i, ref), c2);
             const float2 d = f2_unpack(d2);
             const uint64_t e2 = f2_pack(ex2(d.x), ex2(d.y));
             if (CLAMP) d2 = f2_pack(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f));
@@ -463,9 +464,7 @@ __global__ void __launch_bounds__(kTlThreads, kTlBlocks) token_logprobs_kernel(c
             tl_max[local * kTlThreads + tid] = tl_keep(gm);
             if (piece * kPiece + kGroup * tid < p.V) thread_best = fmaxf(thread_best, gm);
         }
-        float m = gm;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float m = warp_max(gm);
         const float ref = m == kNegInf ? 0.0f : m;
         float s, t;
         if (!masked) {
