@@ -2,7 +2,7 @@
 // sequence).
 //
 // The cache is pages of P tokens; a sequence's block table names its pages in order.  A sequence of up to
-// kPgWhole tokens is one split (no second launch: with splits of 256 the 5.6 us of 300 tokens were 1 us more), a
+// kPgWhole tokens is one split (no second launch: with splits of 256 the 5.5 us of 300 tokens were 1 us more), a
 // longer one is cut into splits of kPgSplit tokens, and each split into tiles of kPgTile tokens: cuts fixed by
 // the sequence's own length.  A (split, kv head) is taken by a group of four warps: warp w takes tiles w,
 // w + 4, ..., with a running maximum; scores, weights and the weighted value sum never leave the warp.
@@ -10,8 +10,8 @@
 // at once, the splits of a longer one go to scratch and are folded by the second launch in a tree fixed
 // by the number of splits.  So a sequence's output depends on its own query, tokens and length only.
 //
-// Bound by the cache's bytes (B200: 64 sequences of 4096 tokens, 32 / 8 heads of 128, pages of 16, 174 us or
-// 6.2 TB/s; 256 of 512 tokens 81.9 us, 6.6 TB/s) and, for a few short sequences, by latency: prefix sums, page
+// Bound by the cache's bytes (B200: 64 sequences of 4096 tokens, 32 / 8 heads of 128, pages of 16, 170 us or
+// 6.3 TB/s; 256 of 512 tokens 81.7 us, 6.6 TB/s) and, for a few short sequences, by latency: prefix sums, page
 // table and first tile take about 2 us, a tile 0.7 us, the fold 0.7 us.  One persistent CTA per SM; the (split, kv head) items of the batch are
 // numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
 // how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the

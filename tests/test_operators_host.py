@@ -18,6 +18,7 @@ NULL = None
 @pytest.fixture(scope="module")
 def lib():
     libbuild.build()
+    libbuild.build_marshal()
     return binding.load()
 
 
@@ -184,3 +185,12 @@ def test_binding_refuses_cpu_tensors():
         binding.bi_paged_decode_attention(x, c, c, n.view(2, 1), n)
     with pytest.raises(ValueError):
         binding.bi_token_logprobs(torch.zeros(2, 8))
+
+
+def test_missing_extension_module_fails_loudly(monkeypatch):
+    import sys
+    monkeypatch.setattr(binding, "_marshal", None)
+    monkeypatch.setitem(sys.modules, "invariant_bi_matmul_02_b200._marshal", None)
+    monkeypatch.delattr(sys.modules["invariant_bi_matmul_02_b200"], "_marshal", raising=False)
+    with pytest.raises(RuntimeError, match="_marshal.so"):
+        binding.load_marshal()
