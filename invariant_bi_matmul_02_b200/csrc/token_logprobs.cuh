@@ -12,7 +12,7 @@
 // row's maximum, lane j adds triples j, j + 32, ... in order, then a fixed butterfly.  A row is taken by one block or
 // by a cluster of 2, 4 or 8 that share its pieces; the triples, and so the bits, are the same.
 //
-// Many rows are bound by memory and by the issue slots (2.5 of 4 instructions a cycle, beside the special-function
+// Many rows are bound by memory and by the issue slots (2.4 of 4 instructions a cycle, beside the special-function
 // unit's half): 1024 rows of 151936 bf16 take 53 us, 5.9 TB/s, and fp32 96 us, 6.5 TB/s; with the 5 best 59 and
 // 103.  One row is bound by latency: 5.1 us, 8.2 with the 20 best.
 //
