@@ -8,6 +8,7 @@
 // pieces), which never changes a row's arithmetic.
 #include "bi.h"
 
+#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -548,24 +549,66 @@ inline int64_t rope_steps(int64_t H, int64_t D, int64_t R, int64_t W)
     return turned > copied ? turned : copied > 0 ? copied : 1;
 }
 
+// The launch: warps that share a token, and how many of its steps a warp has in shared memory at once (0 where
+// the walk is not streamed).
+struct RopeLaunch {
+    int shares, stages;
+    dim3 grid;
+    size_t smem;
+    RopeLaunch(int64_t T, int64_t steps, bool streamed, int R, int sms)
+    {
+        steps = std::max<int64_t>(steps, 1);
+        shares = rope_shares(T, steps, sms);
+        const int64_t mine = (steps + shares - 1) / shares;
+        stages = !streamed ? 0 : (int)(mine < bi::kRopeStages ? mine : bi::kRopeStages);
+        grid = dim3((unsigned)((T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps));
+        smem = (size_t)bi::kRopeWarps * (stages * 1024 + R * sizeof(float));
+        // Launched while the kernel before it still holds places, a grid that fits the GPU at once would sit unevenly, up to
+        // kRopeBlocks on one SM and few on another.  A request for more shared memory than an SM has for one block above
+        // its share keeps the blocks apart (512 tokens appended 6.6 us without, 5.5 with; 3001 tokens of 13 heads of 96
+        // fp32 turned 7.6 and 7.1).  Fewer than four a SM would ask for more than 48 KB a block.
+        const int64_t per_sm = ((int64_t)grid.x + sms - 1) / sms;
+        if (per_sm >= 4 && per_sm < bi::kRopeBlocks)
+            smem = std::max<size_t>(smem, (size_t)(228 * 1024 / (per_sm + 1) - 1024 + 512));  // 1 KB a block is the system's
+    }
+};
+
+template <typename E, int W, bool STREAM>
+bi_status launch_rope(const bi::RopeParams &p, bool half, const RopeLaunch &l, cudaStream_t s)
+{
+    const dim3 block(bi::kRopeThreads);
+    return half ? launch_pdl(bi::rope_kernel<E, W, true, STREAM>, l.grid, block, l.smem, s, p, l.shares, l.stages)
+                : launch_pdl(bi::rope_kernel<E, W, false, STREAM>, l.grid, block, l.smem, s, p, l.shares, l.stages);
+}
+
 template <typename E, int W>
 bi_status launch_rope(const bi::RopeParams &p, bool half, int sms, cudaStream_t s)
 {
-    const int shares = rope_shares(p.T, rope_steps(p.H, p.D, p.R, W), sms);
-    const dim3 grid((unsigned)((p.T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps)), block(bi::kRopeThreads);
-    const size_t smem = (size_t)bi::kRopeWarps * (p.R / 2) * sizeof(float2);
-    return half ? launch_pdl(bi::rope_kernel<E, W, true>, grid, block, smem, s, p, shares)
-                : launch_pdl(bi::rope_kernel<E, W, false>, grid, block, smem, s, p, shares);
+    if constexpr (sizeof(bi::Piece<E, W>) == 16) {
+        // A streamed walk costs 0.3 us more to begin and pays for it where warps have many steps to take (streamed and
+        // through registers: one token 2.4 and 2.1, 1024 tokens of 40 heads 6.0 and 5.2, 1200 of 8 heads 3.5 and 3.1;
+        // 1500 of 40 heads 7.3 and 7.5, 2048 10.2 and 11.1, 4096 of 16 heads 7.8 and 10.2) or where it takes copied
+        // entries along (64 tokens, half of each head turned: 2.6 and 3.1).
+        const int rest = p.copy_piece == 16 ? p.D - p.R : 0;
+        const RopeLaunch l(p.T, bi::RopeSteps<W>(p.R, rest).steps(p.H), true, p.R, sms);
+        if (rest > 0 || p.T >= 12 * sms) return launch_rope<E, W, true>(p, half, l, s);
+    }
+    return launch_rope<E, W, false>(p, half, RopeLaunch(p.T, rope_steps(p.H, p.D, p.R, W), false, p.R, sms), s);
 }
 
 template <int W>
 bi_status launch_append(const bi::AppendParams &p, bool half, int sms, cudaStream_t s)
 {
-    const int shares = rope_shares(p.T, rope_steps((p.q ? p.Hq : 0) + p.Hkv, p.D, p.R, W), sms);
-    const dim3 grid((unsigned)((p.T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps)), block(bi::kRopeThreads);
-    const size_t smem = (size_t)bi::kRopeWarps * (p.R / 2) * sizeof(float2);
-    return half ? launch_pdl(bi::paged_append_kernel<W, true>, grid, block, smem, s, p, shares)
-                : launch_pdl(bi::paged_append_kernel<W, false>, grid, block, smem, s, p, shares);
+    const bi::RopeSteps<W> shape(p.R, bi::append_rest<W>(p));
+    const int64_t Hq = p.q ? p.Hq : 0;
+    const bool streamed = W == 8 && shape.units > 0;
+    const int64_t steps =
+        streamed ? (int64_t)shape.steps((int)Hq) + shape.steps(p.Hkv) + (bi::append_values<W>(p) ? shape.steps(p.Hkv) : 0)
+                 : rope_steps(Hq + p.Hkv, p.D, p.R, W);
+    const RopeLaunch l(p.T, steps, streamed, p.R, sms);
+    const dim3 block(bi::kRopeThreads);
+    return half ? launch_pdl(bi::paged_append_kernel<W, true>, l.grid, block, l.smem, s, p, l.shares, l.stages)
+                : launch_pdl(bi::paged_append_kernel<W, false>, l.grid, block, l.smem, s, p, l.shares, l.stages);
 }
 
 // A cache description that the paged entry points take.
@@ -961,7 +1004,7 @@ bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, 
     p.scale = scale;
     p.inverse = inverse ? 1 : 0;
     // Pieces of 16 bytes, two entries or one, as sizes, strides and addresses allow (8284 tokens of 19 heads of 192, 74
-    // entries turned: 58 us by single entries; 20 turned: 38 by twos).
+    // entries turned: 47 us by single entries; 20 turned: 31 by twos).
     const int64_t entry = bf16 ? 2 : 4;
     auto strided = [&](int64_t W) { return strided_pieces(W, entry, x, xt, xh) && strided_pieces(W, entry, y, yt, yh); };
     auto fits = [&](int64_t W) { return R / 2 % W == 0 && strided(W); };

@@ -8,14 +8,16 @@
 // each output is one fp32 expression rounded once.  The work is elementwise, so every launch shape
 // gives the same bits.
 //
-// Bound by memory for many tokens (B200: 40 heads of 128 of 8192 tokens, bf16, 31.2 us or 5.4 TB/s; 9734 tokens
-// appended with 32 query and 8 key and value heads 46 us, 5.2 TB/s) and by latency for few (one token 2.1 us, 64 appended 4.0).  A warp takes a token (or a share of its heads
-// where there are few tokens): it works out the token's R/2 sines and cosines once, into its own piece of
-// shared memory, and its lanes keep a fixed place in the head while they walk the heads.  A lane's unit
-// is W entries a and their W partners b (16-byte pieces where sizes, strides and addresses allow it, else two
-// entries or one; the arithmetic is the same).  A lane's next head is on its way while one is turned, and
-// the first is before the angles are worked out.  Entries that are only copied are moved apart from the
-// pairs, in the widest pieces that they allow.
+// Bound by memory for many tokens (B200: 40 heads of 128 of 8192 tokens, bf16, 28.9 us or 5.8 TB/s; 9734 tokens
+// appended with 32 query and 8 key and value heads 42.5 us, 5.6 TB/s) and by latency for few (one token 2.1 us, 64
+// appended 3.8).  A warp takes a token (or a share of its heads where there are few tokens): it works out the token's R/2
+// sines and cosines once, into its own piece of shared memory, and its lanes keep a fixed place in the head while
+// they walk the heads.  A lane's unit is W entries a and their W partners b (16-byte pieces where sizes, strides and
+// addresses allow it, else two entries or one; the arithmetic is the same).
+// Walks of 16-byte pieces are streamed: copies to shared memory bring up to kRopeStages steps of the queries, the keys
+// and the values at once, with entries that are only copied as units of their own, so that most of a token's 10 KB is
+// on its way while the angles are worked out (with two steps in registers instead: 31.2 and 45.8 us).  Narrower
+// pieces go through registers, and the entries that are only copied go apart, in the widest pieces that they allow.
 #pragma once
 
 #include <cstdint>
@@ -27,7 +29,7 @@
 namespace bi {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBlocks = 6;      // resident per SM, a bound on registers
+constexpr int kRopeBlocks = 7;  // resident per SM, a bound on registers (4096 x 40 x 128: 17.5 us with 6, 15.5 with 7)
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 16 KB
 constexpr int kRopeCopies = 4;     // value pieces a lane has in flight
@@ -46,9 +48,9 @@ struct alignas(2 * sizeof(E)) Piece<E, 2> {
     E e[2];
 };
 
-// A lane's buffers: one head is turned while the others are on their way.  More for smaller pieces, as registers
-// allow (8284 tokens of 19 heads of 192, 74 bf16 entries turned one by one: 57.7 us with 6, 88.8 with 2; 20 by
-// twos: 35.2 with 4, 37.8 with 2; 16-byte pieces of 8192 x 40 x 128: 31.4 with 2, 32.5 with 3).
+// Buffers of a lane that walks through registers: one head is turned while the others are on their way.  More for
+// smaller pieces, as registers allow (8284 tokens of 19 heads of 192, 74 bf16 entries turned one by one: 88.8 us with 2,
+// 57.7 with 6; 20 by twos: 37.8 with 2, 35.2 with 4; both before kRopeBlocks was 7, 46.5 and 30.8 since).
 template <typename E, int W>
 __host__ __device__ constexpr int rope_buffers()
 {
@@ -71,25 +73,34 @@ __device__ __forceinline__ void rope_angle(int32_t pos, double inv_freq, float s
     s = __fmul_rn(s, scale);
 }
 
-// The cosines, sines and negated sines of a unit's W pairs.
+// The cosines and sines of a unit's W pairs.
 template <int W>
 struct RopeTurn {
-    float c[W], s[W], n[W];
+    float c[W], s[W];
     __device__ __forceinline__ void load(const float *cs, int half, int pair)
     {
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             c[j] = cs[pair + j];
             s[j] = cs[half + pair + j];
-            n[j] = -s[j];
+        }
+    }
+    // The first half of the pairs from `pair` on, the second from `pair2` on.
+    __device__ __forceinline__ void load2(const float *cs, int half, int pair, int pair2)
+    {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int at = j < W / 2 ? pair + j : pair2 + j - W / 2;
+            c[j] = cs[at];
+            s[j] = cs[half + at];
         }
     }
     // Pairs j and j + 1: (x, y) to (x c - y s, y c + x s), each one product and one fused sum.
     __device__ __forceinline__ void turn2(int j, uint64_t &x, uint64_t &y) const
     {
         const uint64_t c2 = f2_pack(c[j], c[j + 1]);
-        const uint64_t u = f2_fma(x, c2, f2_mul(y, f2_pack(n[j], n[j + 1])));
-        y = f2_fma(y, c2, f2_mul(x, f2_pack(s[j], s[j + 1])));
+        const uint64_t s2 = f2_pack(s[j], s[j + 1]), u = f2_fma(x, c2, f2_mul(y, s2) ^ 0x8000000080000000ull);
+        y = f2_fma(y, c2, f2_mul(x, s2));
         x = u;
     }
 };
@@ -101,7 +112,7 @@ __device__ __forceinline__ void rope_unit(Piece<E, W> &a, Piece<E, W> &b, const 
 {
     if constexpr (W == 1) {
         const float x = to_f32(a.e), y = to_f32(b.e);
-        from_f32(__fmaf_rn(x, t.c[0], __fmul_rn(y, t.n[0])), a.e);
+        from_f32(__fmaf_rn(x, t.c[0], -__fmul_rn(y, t.s[0])), a.e);
         from_f32(__fmaf_rn(y, t.c[0], __fmul_rn(x, t.s[0])), b.e);
     } else if constexpr (W == 2) {
         E &x0 = a.e[0], &x1 = HALF ? a.e[1] : b.e[0], &y0 = HALF ? b.e[0] : a.e[1], &y1 = b.e[1];
@@ -163,6 +174,127 @@ struct RopeLane {
         if (head >= heads) unit = units;
     }
 };
+
+// Steps of a warp that a streamed walk has on their way at once (8192 x 40 x 128: 29.3 us with 4, 28.9 with 6; 8 and 10
+// leave room for fewer warps: 29.3, 30.6).
+constexpr int kRopeStages = 6;
+
+// One of a token's tensors (queries, keys or values) in a streamed walk: H heads, src_head and dst_head entries apart.
+template <typename E>
+struct RopeStretch {
+    const E *src;
+    int64_t src_head, dst_head;
+    int H;
+};
+
+// How a streamed walk splits a head and a token: units of 2W entries, the first R/2W turned and the others copied;
+// 32 / units heads to a step (or one head, 32 units at a time); steps numbered through the N stretches.
+template <int W>
+struct RopeSteps {
+    int units, heads;
+    __host__ __device__ RopeSteps(int R, int rest) : units(R / (2 * W) + (rest + 2 * W - 1) / (2 * W))
+    {
+        heads = units > 0 && units < 32 ? 32 / units : 1;
+    }
+    __host__ __device__ int steps(int H) const { return units > 0 ? (H + heads - 1) / heads : 0; }
+};
+
+// Turns (stretches below `turned`) or copies the heads of one token's N stretches, every `shares`-th step from
+// `share` on.  rest: entries R .. R + rest - 1 of each head are copied.  ring: `stages` steps of the warp, each 64
+// pieces; as many as it takes, or kRopeStages if those are fewer.  ready() is called once the first loads are
+// in flight and before cs or dst(i), stretch i's place, is needed; false ends the walk.
+template <typename E, int W, bool HALF, int N, typename Ready, typename Dst>
+__device__ __forceinline__ bool rope_stream(const RopeStretch<E> (&st)[N], int turned, int R, int rest, int share,
+                                            int shares, uint4 *ring, int stages, const float *cs, Ready ready, Dst dst)
+{
+    const RopeSteps<W> shape(R, rest);
+    const int lane = threadIdx.x & 31, half = R / 2, turning = R / (2 * W);
+    int first[N + 1];  // first step of each stretch
+    first[0] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) first[i + 1] = first[i] + shape.steps(st[i].H);
+    if (share >= first[N]) return true;
+    const int mine = (first[N] - share + shares - 1) / shares;
+    for (int u0 = 0; u0 < shape.units; u0 += 32) {
+        const int my_head = shape.units < 32 ? lane / shape.units : 0, u = u0 + lane - my_head * shape.units;
+        const bool on = my_head < shape.heads && u < shape.units, turns = u < turning;
+        // Either layout's piece a is in the first half of the turned (or copied) entries and b in the second, so that
+        // neighbouring lanes have neighbouring pieces.
+        const int ea = turns ? u * W : R + (u - turning) * W, eb = ea + (turns ? half : (shape.units - turning) * W);
+        const bool has_b = turns || eb < R + rest;
+        // Stretch and head that step j of this warp gives the lane; head >= H: none.
+        auto place = [&](int j, int &i, int &h) {
+            const int g = share + j * shares;
+            i = 0;
+            int base = 0;
+#pragma unroll
+            for (int k = 1; k < N; ++k)
+                if (g >= first[k]) {
+                    i = k;
+                    base = first[k];
+                }
+            h = my_head + (g - base) * shape.heads;
+        };
+        auto pick = [&](int i) {  // st[i] without an indexed array
+            RopeStretch<E> v = st[0];
+#pragma unroll
+            for (int k = 1; k < N; ++k)
+                if (i == k) v = st[k];
+            return v;
+        };
+        auto load = [&](int j, int slot) {
+            int i, h;
+            place(j, i, h);
+            const RopeStretch<E> v = pick(i);
+            if (on && h < v.H) {
+                const E *from = v.src + h * v.src_head;
+                cp_async16(ring + slot * 64 + lane, from + ea, 16);
+                if (has_b) cp_async16(ring + slot * 64 + 32 + lane, from + eb, 16);
+            }
+        };
+#pragma unroll 1
+        for (int k = 0; k < stages && k < mine; ++k) {
+            load(k, k);
+            cp_async_commit();
+        }
+        if (!ready()) {
+            cp_async_wait_all();
+            return false;
+        }
+        RopeTurn<W> turn;
+        if (on && turns) HALF ? turn.load(cs, half, u * W) : turn.load2(cs, half, u * (W / 2), (half + u * W) / 2);
+        int slot = 0;
+#pragma unroll 1
+        for (int j = 0; j < mine; ++j) {
+            // Steps j .. min(j + stages, mine) - 1 are on their way.
+            const int left = mine - j;
+            if (left >= kRopeStages)
+                cp_async_wait_pending<kRopeStages - 1>();
+            else if (left >= kRopeStages / 2)
+                cp_async_wait_pending<kRopeStages / 2 - 1>();
+            else
+                cp_async_wait_pending<0>();
+            Piece<E, W> a, b;
+            *reinterpret_cast<uint4 *>(&a) = ring[slot * 64 + lane];
+            *reinterpret_cast<uint4 *>(&b) = ring[slot * 64 + 32 + lane];
+            if (j + stages < mine) {
+                load(j + stages, slot);
+                cp_async_commit();
+            }
+            slot = slot + 1 == stages ? 0 : slot + 1;
+            int i, h;
+            place(j, i, h);
+            const RopeStretch<E> v = pick(i);
+            if (on && h < v.H) {
+                if (turns && i < turned) rope_unit<E, W, HALF>(a, b, turn);
+                E *to = dst(i) + h * v.dst_head;
+                *reinterpret_cast<Piece<E, W> *>(to + ea) = a;
+                if (has_b) *reinterpret_cast<Piece<E, W> *>(to + eb) = b;
+            }
+        }
+    }
+    return true;
+}
 
 // The warp's token's R/2 cosines, then R/2 sines, into cs.
 __device__ __forceinline__ void rope_angles(float *cs, const double *inv_freq, int half, int32_t pos, float scale, bool inverse)
@@ -274,32 +406,41 @@ struct RopeParams {
     int32_t copy_piece;  // bytes; 0: entries R .. D-1 are not copied (none, or y is x)
 };
 
-// `shares` warps take a token's heads in turn.
-template <typename E, int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p, int shares)
+// `shares` warps take a token's heads in turn, in a streamed walk or not.  (Two 16-byte buffers want more registers: 512
+// tokens 4.3 us with kRopeBlocks, 3.8 with 6.)
+template <typename E, int W, bool HALF, bool STREAM>
+__global__ void __launch_bounds__(kRopeThreads, !STREAM && sizeof(Piece<E, W>) == 16 ? 6 : kRopeBlocks)
+    rope_kernel(const RopeParams p, int shares, int stages)
 {
-    extern __shared__ __align__(16) float rope_cs[];  // [kRopeWarps][R]
-    float *cs = rope_cs + (threadIdx.x >> 5) * p.R;
-    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
+    extern __shared__ __align__(16) uint8_t rope_smem[];  // [kRopeWarps][stages][64] pieces, [kRopeWarps][R] floats
+    const int warp = threadIdx.x >> 5;
+    uint4 *ring = reinterpret_cast<uint4 *>(rope_smem) + warp * stages * 64;
+    float *cs = reinterpret_cast<float *>(rope_smem + kRopeWarps * stages * 1024) + warp * p.R;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp, t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
-    const RopeLane<W> me(p.R);
     const int share = (int)(gw - t * shares);
     const E *x = static_cast<const E *>(p.x) + t * p.x_token;
     E *y = static_cast<E *>(p.y) + t * p.y_token;
     bool have = false;
-    rope_walk<E, W, HALF>(
-        me, x, p.x_head, p.y_head, p.H, p.R, share, shares, cs,
-        [&] {
-            if (!have) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
-            have = true;
-            return true;
-        },
-        [&] { return y; });
-    if (p.copy_piece)
+    auto ready = [&] {
+        if (!have) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
+        have = true;
+        return true;
+    };
+    int copy_piece = p.copy_piece;
+    if constexpr (STREAM) {
+        const RopeStretch<E> st[1] = {{x, p.x_head, p.y_head, p.H}};
+        rope_stream<E, W, HALF>(st, 1, p.R, copy_piece == 16 ? p.D - p.R : 0, share, shares, ring, stages, cs, ready,
+                                [&](int) { return y; });
+        if (copy_piece == 16) copy_piece = 0;
+    } else {
+        rope_walk<E, W, HALF>(RopeLane<W>(p.R), x, p.x_head, p.y_head, p.H, p.R, share, shares, cs, ready, [&] { return y; });
+    }
+    if (copy_piece)
         copy_heads(
-            p.copy_piece, x + p.R, p.x_head * (int)sizeof(E), p.y_head * (int)sizeof(E), p.H, (p.D - p.R) * (int)sizeof(E),
+            copy_piece, x + p.R, p.x_head * (int)sizeof(E), p.y_head * (int)sizeof(E), p.H, (p.D - p.R) * (int)sizeof(E),
             share, shares, [] { return true; }, [&] { return reinterpret_cast<uint8_t *>(y + p.R); });
 }
 
@@ -363,19 +504,32 @@ __device__ __forceinline__ AppendPlace append_place(const AppendParams &p, int64
     return {at, b, page};
 }
 
+// What a streamed walk of 16-byte pieces takes with it: the entries that are only copied, and the values.
+template <int W>
+__host__ __device__ inline int append_rest(const AppendParams &p)
+{
+    return W == 8 && p.rest_piece == 16 ? p.D - p.R : 0;
+}
+template <int W>
+__host__ __device__ inline bool append_values(const AppendParams &p)
+{
+    return W == 8 && p.v_piece == 16 && p.R + append_rest<W>(p) == p.D;
+}
+
 // `shares` warps take a token's query heads, key heads and values in turn.
 template <int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel(const AppendParams p, int shares)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel(const AppendParams p, int shares, int stages)
 {
     using E = __nv_bfloat16;
-    extern __shared__ __align__(16) float rope_cs[];  // [kRopeWarps][R]
-    float *cs = rope_cs + (threadIdx.x >> 5) * p.R;
-    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5), t = gw / shares;
+    extern __shared__ __align__(16) uint8_t rope_smem[];  // as in rope_kernel
+    const int warp = threadIdx.x >> 5;
+    uint4 *ring = reinterpret_cast<uint4 *>(rope_smem) + warp * stages * 64;
+    float *cs = reinterpret_cast<float *>(rope_smem + kRopeWarps * stages * 1024) + warp * p.R;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp, t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
     const int share = (int)(gw - t * shares);
-    const RopeLane<W> me(p.R);
     int64_t row = -1;  // offset of the token's row in the cache (head 0), or -1: the token is skipped
     bool have = false;
     auto ready = [&] {
@@ -396,25 +550,38 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
     E *qo = p.q_out + t * p.qo_token;
     auto bytes_at = [](E *e) { return reinterpret_cast<uint8_t *>(e); };
     constexpr int kE = sizeof(E);
-    int group = share;  // the warp's next group of heads; the key heads go on where the query heads end
-    if (p.q != nullptr) {
-        if (!rope_walk<E, W, HALF>(me, q, p.q_head, p.qo_head, p.Hq, p.R, group, shares, cs, ready, [&] { return qo; })) return;
-        group = (share + shares - (p.Hq + me.heads - 1) / me.heads % shares) % shares;
+    int rest = p.rest_piece ? p.D - p.R : 0;  // entries left to copy after the walk
+    if constexpr (W == 8) {
+        const RopeStretch<E> st[3] = {{q, p.q_head, p.qo_head, p.q != nullptr ? p.Hq : 0},
+                                      {k, p.k_head, p.c_head, p.Hkv},
+                                      {v, p.v_head, p.c_head, append_values<W>(p) ? p.Hkv : 0}};
+        if (!rope_stream<E, W, HALF>(st, 2, p.R, append_rest<W>(p), share, shares, ring, stages, cs, ready,
+                                     [&](int i) { return i == 0 ? qo : (i == 1 ? p.k_cache : p.v_cache) + row; }))
+            return;
+        rest -= append_rest<W>(p);
+    } else {
+        const RopeLane<W> me(p.R);
+        int group = share;  // the warp's next group of heads; the key heads go on where the query heads end
+        if (p.q != nullptr) {
+            if (!rope_walk<E, W, HALF>(me, q, p.q_head, p.qo_head, p.Hq, p.R, group, shares, cs, ready, [&] { return qo; }))
+                return;
+            group = (share + shares - (p.Hq + me.heads - 1) / me.heads % shares) % shares;
+        }
+        if (!rope_walk<E, W, HALF>(me, k, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, ready,
+                                   [&] { return p.k_cache + row; }))
+            return;
     }
-    if (!rope_walk<E, W, HALF>(me, k, p.k_head, p.c_head, p.Hkv, p.R, group, shares, cs, ready,
-                               [&] { return p.k_cache + row; }))
-        return;
-    if (p.rest_piece) {
-        const int rest = (p.D - p.R) * kE;
-        if (p.q != nullptr && !copy_heads(p.rest_piece, q + p.R, p.q_head * kE, p.qo_head * kE, p.Hq, rest, share, shares,
+    if (rest > 0) {
+        if (p.q != nullptr && !copy_heads(p.rest_piece, q + p.R, p.q_head * kE, p.qo_head * kE, p.Hq, rest * kE, share, shares,
                                           ready, [&] { return bytes_at(qo + p.R); }))
             return;
-        if (!copy_heads(p.rest_piece, k + p.R, p.k_head * kE, p.c_head * kE, p.Hkv, rest, share, shares, ready,
+        if (!copy_heads(p.rest_piece, k + p.R, p.k_head * kE, p.c_head * kE, p.Hkv, rest * kE, share, shares, ready,
                         [&] { return bytes_at(p.k_cache + row + p.R); }))
             return;
     }
-    copy_heads(p.v_piece, v, p.v_head * kE, p.c_head * kE, p.Hkv, p.D * kE, share, shares, ready,
-               [&] { return bytes_at(p.v_cache + row); });
+    if (!append_values<W>(p))
+        copy_heads(p.v_piece, v, p.v_head * kE, p.c_head * kE, p.Hkv, p.D * kE, share, shares, ready,
+                   [&] { return bytes_at(p.v_cache + row); });
 }
 
 }  // namespace bi

@@ -481,3 +481,30 @@ def test_a_prefill_and_decode_steps_together():
         assert same_bits(kc[table[b].long()[rows // page], rows % page], dense)
         assert same_bits(generate([b], 300 + b)[0], outs[b:b + 1])
     assert bi.bi_get_device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("Hq,Hkv,D,R", [(24, 7, 128, 128), (20, 5, 64, 32), (0, 9, 128, 96), (9, 3, 72, 48), (5, 2, 96, 0),
+                                        (3, 1, 1024, 1024)])
+def test_append_long_prompts_take_one_warp_per_token(Hq, Hkv, D, R, layout):
+    """A warp walks a whole token's queries, keys and values: more steps than it has on its way at once."""
+    g = gen(Hq + D)
+    lens, cu, page = [2000, 600, 0, 40], [0, 1990, 2590, 2590, 2600], 16
+    T, pages = 2603, 200
+    kc, vc = make_cache(g, pages, page, Hkv, D)
+    table = make_table(g, lens, page, pages)
+    sl, c = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, cu))
+    k, v = (torch.randn(T, Hkv, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T, Hq, D, generator=g, device=DEV).to(torch.bfloat16) if Hq else None
+    f = bi.bi_rope_freqs(R, 1e5)[0] if R else None
+    scale = 1.1 if R else 1.0
+    before_k, before_v = kc.clone(), vc.clone()
+    q_out = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV) if Hq else None
+    bi.bi_paged_append(k, v, kc, vc, table, sl, c, f, layout, scale, q, q_out)
+    wk, wv, at, row, t, _, _, pos = append_definition(k, v, before_k, before_v, table, lens, cu, f, layout, scale, q, None, None)
+    turned = lambda x: bi.bi_rope(x[t], pos.to(torch.int32), f, layout, scale) if R else x[t]
+    wk[at, row], wv[at, row] = turned(k), v[t]
+    assert same_bits(kc.contiguous(), wk.contiguous()) and same_bits(vc.contiguous(), wv.contiguous())
+    if Hq:
+        assert same_bits(q_out[t], turned(q)) and bool((q_out[2600:] == 7.0).all())
+    assert bi.bi_get_device_status() == bi.BI_OK

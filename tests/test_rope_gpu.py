@@ -156,3 +156,24 @@ def test_rope_binding_refusals():
             bad()
     with pytest.raises(bi.BiError):
         bi.bi_rope(x[..., :4], pos, f)  # R = 8 > D = 4
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D,R", [
+    (2369, 75, 64, 64),     # more steps a warp than it has on its way at once, the last not full
+    (1300, 61, 128, 96),    # two warps a token, some units turned and some copied
+    (2400, 9, 200, 176),    # an odd number of copied pieces
+    (2400, 5, 100, 96),     # the same in fp32
+    (2400, 3, 1024, 1024),  # heads of more than 32 units
+    (1200, 3, 1024, 16),
+    (2400, 7, 80, 0),       # nothing turned
+])
+def test_rope_streamed_walks(T, H, D, R, dtype, layout):
+    x, pos, f = make(T + H, T, H, D, R, dtype, start=5000)
+    y = bi.bi_rope(x, pos, f, layout, 0.75)
+    check(y, x, pos, f, layout, 0.75, False)
+    some = torch.tensor([0, 1, T // 2, T - 1], device=DEV)
+    assert same_bits(bi.bi_rope(x[some], pos[some], f, layout, 0.75), y[some])  # few tokens: other walks, the same bits
+    z = x.clone()
+    assert same_bits(bi.bi_rope(z, pos, f, layout, 0.75, out=z), y)
