@@ -80,6 +80,10 @@ bi_status paged_smem_opt_in()
 // Shared memory of a token_logprobs block that takes `pieces` pieces.
 inline size_t token_logprobs_smem(int64_t pieces, int64_t top) { return top > 0 ? (size_t)pieces * bi::kTlThreads * sizeof(uint16_t) : 0; }
 
+// With this much and its own 14.5 KB a block takes more than a quarter of an SM's 228 KB, and less than a third.
+constexpr int kTlThirdOfSm = 43 * 1024;
+static_assert(kTlThirdOfSm >= bi::kTlMaxPieces * bi::kTlThreads * (int)sizeof(uint16_t), "the longest row's group maxima fit");
+
 bi_status token_logprobs_smem_opt_in()
 {
     const void *fns[4] = {reinterpret_cast<const void *>(bi::token_logprobs_kernel<true, true>),
@@ -87,8 +91,7 @@ bi_status token_logprobs_smem_opt_in()
                           reinterpret_cast<const void *>(bi::token_logprobs_kernel<false, true>),
                           reinterpret_cast<const void *>(bi::token_logprobs_kernel<false, false>)};
     for (const void *fn : fns)
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)token_logprobs_smem(bi::kTlMaxPieces, 1)) != cudaSuccess)
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTlThirdOfSm) != cudaSuccess)
             return BI_ERR_CUDA;
     return BI_OK;
 }
@@ -1267,14 +1270,26 @@ bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const 
     p.top_logprobs = top_logprobs;
     p.top_tokens = top_tokens;
     p.status = dev->status;
-    // Blocks that share a row: as many as leave the GPU 2 blocks an SM (top 8 of 64 rows of 151936 bf16: 10.9 us with
-    // clusters of 4, 13.2 with 8, which fill it), or 3.5 where rows are longer than 384 KB and each block's share
-    // counts for more (160 rows of 151936 fp32: 26.0 us with clusters of 2, 32.8 alone).  Never all 4:
-    // clusters do not pack, and a few rows would run after the rest (148 rows of bf16: 21.2 against 16.1 us).
-    const int64_t row_bytes = V * (bf16 ? 2 : 4), most = (row_bytes > 384 * 1024 ? 7 : 4) * (int64_t)dev->sms / 2;
+    // Blocks that share a row: as many as fit the GPU at once with room to spare.  Clusters of 8 up to 2 blocks an SM
+    // (top 8 of 64 rows of 151936 bf16: 10.9 us with clusters of 4, 13.2 with 8); of 4 up to 2.8 and of 2 up to 3, if
+    // each block has two pieces to take (top 5, with one block a row less and so: 100 rows 14.9 and 13.2 us, 200 rows 22.1
+    // and 19.0; clusters of 4 do not pack closer, and the last run after the rest: 108 rows 14.9 and 18.3), else 2; any
+    // up to 3.5 where rows are longer than 384 KB and each block's share counts for more (160 rows of 151936 fp32: 26.0
+    // us with clusters of 2, 32.8 alone).
+    const int64_t sms = dev->sms, row_bytes = V * (bf16 ? 2 : 4);
+    auto fit = [&](int64_t blocks, int cluster) {
+        if (row_bytes > 384 * 1024) return 2 * blocks <= 7 * sms;
+        if (cluster == 8 || p.pieces < 2 * cluster) return blocks <= 2 * sms;
+        return cluster == 4 ? 5 * blocks <= 14 * sms : blocks <= 3 * sms;
+    };
     p.cluster = bi::kTlMaxCluster;
-    while (p.cluster > 1 && (p.cluster > p.pieces || M * p.cluster > most)) p.cluster /= 2;
-    const size_t smem = token_logprobs_smem((p.pieces + p.cluster - 1) / p.cluster, top_k);
+    while (p.cluster > 1 && (p.cluster > p.pieces || !fit(M * p.cluster, p.cluster))) p.cluster /= 2;
+    size_t smem = token_logprobs_smem((p.pieces + p.cluster - 1) / p.cluster, top_k);
+    // With more than 2 blocks an SM and at most 3, ask for so much shared memory that no SM takes a fourth while the
+    // launch before leaves others short (300 rows of 151936 bf16, top 5: 33.3 us without, 29.0 with).
+    const int64_t blocks = M * p.cluster;
+    if (blocks > 2 * sms && blocks <= 3 * sms && (p.cluster <= 2 || (p.cluster == 4 && 5 * blocks <= 14 * sms)))
+        smem = std::max<size_t>(smem, kTlThirdOfSm);
     const bool vec = aligned16(x) && (M == 1 || ldx % (bf16 ? 8 : 4) == 0);
     void (*kernel)(bi::TlParams) = bf16 ? (vec ? bi::token_logprobs_kernel<true, true> : bi::token_logprobs_kernel<true, false>)
                                         : (vec ? bi::token_logprobs_kernel<false, true> : bi::token_logprobs_kernel<false, false>);

@@ -229,3 +229,18 @@ def test_log_softmax_agrees():
     got = bi.bi_token_logprobs(x, t, 4)
     assert float((y.gather(1, t.long()[:, None])[:, 0] - got.logprobs).abs().max()) <= 1e-4
     assert float((y.gather(1, got.top_tokens.long()) - got.top_logprobs).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-math.inf, -1e30, -1e4, 0.0])
+@pytest.mark.parametrize("M,V,kept", [(1, 50257, 40), (5, 50257, 3), (3, 9000, 700), (90, 50257, 100), (170, 40000, 8),
+                                      (330, 20000, 15)])
+def test_few_tokens_clear_of_a_mask(M, V, kept, low, dtype):
+    """Blocks of a row in which fewer than k threads have a token that the mask left, at every cluster size."""
+    x, _ = rows(V + kept, M, V, dtype)
+    g = torch.Generator(device=DEV).manual_seed(kept)
+    at = torch.rand(M, V, generator=g, device=DEV).topk(kept, dim=1)[1]
+    y = torch.full_like(x, low)
+    y.scatter_(1, at, x.gather(1, at).abs() + 1)
+    check(y, at[:, 0].to(torch.int32), 0.9, 8)
+    check(y, at[:, 0].to(torch.int32), 0.9, 32)
