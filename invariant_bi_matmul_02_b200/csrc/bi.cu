@@ -584,6 +584,14 @@ bi_status launch_rope(const bi::RopeParams &p, bool half, const RopeLaunch &l, c
                 : launch_pdl(bi::rope_kernel<E, W, false, STREAM>, l.grid, block, l.smem, s, p, l.shares, l.stages);
 }
 
+template <typename E>
+bi_status launch_rope_staged(const bi::RopeParams &p, bool half, const RopeLaunch &l, cudaStream_t s)
+{
+    const dim3 block(bi::kRopeThreads);
+    return half ? launch_pdl(bi::rope_staged_kernel<E, true>, l.grid, block, l.smem, s, p, l.shares, l.stages)
+                : launch_pdl(bi::rope_staged_kernel<E, false>, l.grid, block, l.smem, s, p, l.shares, l.stages);
+}
+
 template <typename E, int W>
 bi_status launch_rope(const bi::RopeParams &p, bool half, int sms, cudaStream_t s)
 {
@@ -1006,14 +1014,20 @@ bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, 
     p.R = (int32_t)R;
     p.scale = scale;
     p.inverse = inverse ? 1 : 0;
-    // Pieces of 16 bytes, two entries or one, as sizes, strides and addresses allow (8284 tokens of 19 heads of 192, 74
-    // entries turned: 47 us by single entries; 20 turned: 31 by twos).
+    // Pieces of 16 bytes, two entries or one, as sizes, strides and addresses allow.
     const int64_t entry = bf16 ? 2 : 4;
     auto strided = [&](int64_t W) { return strided_pieces(W, entry, x, xt, xh) && strided_pieces(W, entry, y, yt, yh); };
     auto fits = [&](int64_t W) { return R / 2 % W == 0 && strided(W); };
     p.copy_piece = x == y ? 0 : copy_piece(R, D - R, entry, strided);
     const bool half = layout == BI_ROPE_HALF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t W = 16 / entry, pieces = ((x == y ? R : D) + W - 1) / W;
+    if (R > 0 && !fits(W) && D % W == 0 && pieces <= 64 && strided(W)) {
+        p.pieces = (int32_t)pieces;
+        const int64_t heads = 64 / pieces;
+        const RopeLaunch l(T, (H + heads - 1) / heads, true, p.R, dev->sms);
+        return bf16 ? launch_rope_staged<__nv_bfloat16>(p, half, l, s) : launch_rope_staged<float>(p, half, l, s);
+    }
     if (bf16)
         return fits(8)   ? launch_rope<__nv_bfloat16, 8>(p, half, dev->sms, s)
                : fits(2) ? launch_rope<__nv_bfloat16, 2>(p, half, dev->sms, s)

@@ -16,8 +16,9 @@
 // addresses allow it, else two entries or one; the arithmetic is the same).
 // Walks of 16-byte pieces are streamed: copies to shared memory bring up to kRopeStages steps of the queries, the keys
 // and the values at once, with entries that are only copied as units of their own, so that most of a token's 10 KB is
-// on its way while the angles are worked out (with two steps in registers instead: 31.2 and 45.8 us).  Narrower
-// pieces go through registers, and the entries that are only copied go apart, in the widest pieces that they allow.
+// on its way while the angles are worked out (with two steps in registers instead: 31.2 and 45.8 us).  Heads of
+// 16-byte pieces that the pairs do not fill are turned in shared memory (rope_staged_kernel).  Else narrower pieces go
+// through registers, and the entries that are only copied go apart, in the widest pieces that they allow.
 #pragma once
 
 #include <cstdint>
@@ -404,6 +405,7 @@ struct RopeParams {
     float scale;
     int32_t inverse;
     int32_t copy_piece;  // bytes; 0: entries R .. D-1 are not copied (none, or y is x)
+    int32_t pieces;      // rope_staged_kernel: 16-byte pieces of a head that are taken, 64 at most
 };
 
 // `shares` warps take a token's heads in turn, in a streamed walk or not.  (Two 16-byte buffers want more registers: 512
@@ -442,6 +444,81 @@ __global__ void __launch_bounds__(kRopeThreads, !STREAM && sizeof(Piece<E, W>) =
         copy_heads(
             copy_piece, x + p.R, p.x_head * (int)sizeof(E), p.y_head * (int)sizeof(E), p.H, (p.D - p.R) * (int)sizeof(E),
             share, shares, [] { return true; }, [&] { return reinterpret_cast<uint8_t *>(y + p.R); });
+}
+
+// Heads of 16-byte pieces whose R/2 is not a multiple of a piece's entries: the pieces are streamed as they lie, 64 / pieces
+// heads to a step, and the pairs turned in shared memory one by one, across the lanes, before the pieces go out.
+// (8284 tokens of 19 heads of 192 bf16 with 74 entries turned: 25.9 us, 46.5 when lanes read and wrote single entries; 9000
+// of 2 heads of 256, 254 turned: 9.9 and 17.5; 32 heads of 80, 20 turned: one token 2.4 and 2.9, 2048 6.7 and 6.1.)
+template <typename E, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_staged_kernel(const RopeParams p, int shares, int stages)
+{
+    constexpr int W = 16 / (int)sizeof(E);
+    extern __shared__ __align__(16) uint8_t rope_smem[];  // as in rope_kernel
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.R / 2;
+    uint4 *ring = reinterpret_cast<uint4 *>(rope_smem) + warp * stages * 64;
+    float *cs = reinterpret_cast<float *>(rope_smem + kRopeWarps * stages * 1024) + warp * p.R;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp, t = gw / shares;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (t >= p.T) return;
+    const int share = (int)(gw - t * shares), heads = 64 / p.pieces, steps = (p.H + heads - 1) / heads;
+    if (share >= steps) return;
+    const int mine = (steps - share + shares - 1) / shares;
+    const E *x = static_cast<const E *>(p.x) + t * p.x_token;
+    E *y = static_cast<E *>(p.y) + t * p.y_token;
+    int head[2], entry[2];  // of this lane's two pieces in a step
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        head[k] = i / p.pieces;
+        entry[k] = (i - head[k] * p.pieces) * W;
+        if (head[k] >= heads) head[k] = p.H;  // none
+    }
+    auto load = [&](int j, int slot) {
+        const int h0 = (share + j * shares) * heads;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (h0 + head[k] < p.H) cp_async16(ring + slot * 64 + lane + 32 * k, x + (h0 + head[k]) * p.x_head + entry[k], 16);
+    };
+#pragma unroll 1
+    for (int k = 0; k < stages && k < mine; ++k) {
+        load(k, k);
+        cp_async_commit();
+    }
+    rope_angles(cs, p.inv_freq, half, p.pos[t], p.scale, p.inverse != 0);
+    const float per_half = 1.0f / (float)half;
+    int slot = 0;
+#pragma unroll 1
+    for (int j = 0; j < mine; ++j) {
+        const int left = mine - j;  // as in rope_stream
+        if (left >= kRopeStages)
+            cp_async_wait_pending<kRopeStages - 1>();
+        else if (left >= kRopeStages / 2)
+            cp_async_wait_pending<kRopeStages / 2 - 1>();
+        else
+            cp_async_wait_pending<0>();
+        __syncwarp();
+        const int h0 = (share + j * shares) * heads, pairs = min(heads, p.H - h0) * half;
+        E *at = reinterpret_cast<E *>(ring + slot * 64);
+        for (int i = lane; i < pairs; i += 32) {
+            const int h = (int)(((float)i + 0.5f) * per_half), k = i - h * half;  // i < 2^8: exact
+            E *a = at + h * p.pieces * W + (HALF ? k : 2 * k), *b = a + (HALF ? half : 1);
+            const float u = to_f32(*a), v = to_f32(*b), c = cs[k], s = cs[half + k];
+            from_f32(__fmaf_rn(u, c, -__fmul_rn(v, s)), *a);
+            from_f32(__fmaf_rn(v, c, __fmul_rn(u, s)), *b);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (h0 + head[k] < p.H)
+                *reinterpret_cast<uint4 *>(y + (h0 + head[k]) * p.y_head + entry[k]) = ring[slot * 64 + lane + 32 * k];
+        if (j + stages < mine) {
+            load(j + stages, slot);
+            cp_async_commit();
+        }
+        slot = slot + 1 == stages ? 0 : slot + 1;
+    }
 }
 
 // ------------------------------------------------------------------------------- paged append

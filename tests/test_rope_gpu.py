@@ -177,3 +177,20 @@ def test_rope_streamed_walks(T, H, D, R, dtype, layout):
     assert same_bits(bi.bi_rope(x[some], pos[some], f, layout, 0.75), y[some])  # few tokens: other walks, the same bits
     z = x.clone()
     assert same_bits(bi.bi_rope(z, pos, f, layout, 0.75, out=z), y)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D,R", [(1, 32, 80, 20), (2400, 29, 80, 20), (2400, 13, 192, 74), (1203, 5, 512, 510),
+                                     (77, 1, 24, 22), (2, 48, 256, 2), (9, 3, 1024, 1022)])
+def test_rope_pairs_that_fill_no_pieces(T, H, D, R, dtype, layout):
+    x, pos, f = make(T + D + R, T, H, D, R, dtype, start=70000)
+    y = bi.bi_rope(x, pos, f, layout, 1.1, True)
+    check(y, x, pos, f, layout, 1.1, True)
+    off = torch.empty(T * H * D + 1, dtype=dtype, device=DEV)[1:].view(T, H, D)  # no 16-byte alignment
+    off.copy_(x)
+    assert same_bits(bi.bi_rope(off, pos, f, layout, 1.1, True), y)
+    wide = torch.full((T, H, D + 16), 3.0, dtype=dtype, device=DEV)
+    wide[..., :D] = x
+    bi.bi_rope(wide[..., :D], pos, f, layout, 1.1, True, out=wide[..., :D])
+    assert same_bits(wide[..., :D].contiguous(), y) and bool((wide[..., D:] == 3.0).all())
