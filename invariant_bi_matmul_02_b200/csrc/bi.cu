@@ -622,6 +622,15 @@ bi_status launch_append(const bi::AppendParams &p, bool half, int sms, cudaStrea
                 : launch_pdl(bi::paged_append_kernel<W, false>, l.grid, block, l.smem, s, p, l.shares, l.stages);
 }
 
+bi_status launch_append_staged(const bi::AppendParams &p, bool half, int sms, cudaStream_t s)
+{
+    const int64_t heads = 64 / p.pieces, Hq = p.q ? p.Hq : 0;
+    const RopeLaunch l(p.T, (Hq + heads - 1) / heads + 2 * ((p.Hkv + heads - 1) / heads), true, p.R, sms);
+    const dim3 block(bi::kRopeThreads);
+    return half ? launch_pdl(bi::paged_append_kernel<8, true, true>, l.grid, block, l.smem, s, p, l.shares, l.stages)
+                : launch_pdl(bi::paged_append_kernel<8, false, true>, l.grid, block, l.smem, s, p, l.shares, l.stages);
+}
+
 // A cache description that the paged entry points take.
 bi_status check_cache(const bi_paged_cache *c)
 {
@@ -1158,6 +1167,10 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
     p.v_piece = copy_piece(0, D, 2, [&](int64_t W) { return strided_pieces(W, 2, v, p.v_token, p.v_head); });
     const bool half = layout == BI_ROPE_HALF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (R > 0 && !fits(8) && D % 8 == 0 && D <= 512 && turned(8) && p.v_piece == 16) {
+        p.pieces = (int32_t)(D / 8);
+        return launch_append_staged(p, half, dev->sms, s);
+    }
     return fits(8)   ? launch_append<8>(p, half, dev->sms, s)
            : fits(2) ? launch_append<2>(p, half, dev->sms, s)
                      : launch_append<1>(p, half, dev->sms, s);

@@ -297,6 +297,109 @@ __device__ __forceinline__ bool rope_stream(const RopeStretch<E> (&st)[N], int t
     return true;
 }
 
+// The same for heads of 16-byte pieces that their pairs do not fill (R/2 is not a multiple of a piece's entries): the
+// first `pieces` pieces of a head (64 at most) are streamed as they lie, 64 / pieces heads to a step, and the pairs
+// turned in shared memory one by one, across the lanes, before the pieces go out.
+// (8284 tokens of 19 heads of 192 bf16 with 74 entries turned: 25.9 us, 46.5 when lanes read and wrote single entries; 9000
+// of 2 heads of 256, 254 turned: 9.9 and 17.5; 32 heads of 80, 20 turned: one token 2.4 and 2.9, 2048 6.7 and 6.1; 64
+// sequences' tokens appended with 32 query and 32 key and value heads of 80, 20 turned: 3.4 and 5.6.)
+template <typename E, bool HALF, int N, typename Ready, typename Dst>
+__device__ __forceinline__ bool rope_staged(const RopeStretch<E> (&st)[N], int turned, int R, int pieces, int share, int shares,
+                                            uint4 *ring, int stages, const float *cs, Ready ready, Dst dst)
+{
+    constexpr int W = 16 / (int)sizeof(E);
+    const int lane = threadIdx.x & 31, half = R / 2, heads = 64 / pieces;
+    int first[N + 1];  // first step of each stretch
+    first[0] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) first[i + 1] = first[i] + (st[i].H + heads - 1) / heads;
+    if (share >= first[N]) return true;
+    const int mine = (first[N] - share + shares - 1) / shares;
+    int head[2], entry[2];  // of this lane's two pieces in a step
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        head[k] = i / pieces;
+        entry[k] = (i - head[k] * pieces) * W;
+    }
+    // Stretch of step j of this warp and its first head there.
+    auto place = [&](int j, int &h0) {
+        const int g = share + j * shares;
+        int i = 0, base = 0;
+#pragma unroll
+        for (int k = 1; k < N; ++k)
+            if (g >= first[k]) {
+                i = k;
+                base = first[k];
+            }
+        h0 = (g - base) * heads;
+        return i;
+    };
+    auto pick = [&](int i) {  // st[i] without an indexed array
+        RopeStretch<E> v = st[0];
+#pragma unroll
+        for (int k = 1; k < N; ++k)
+            if (i == k) v = st[k];
+        return v;
+    };
+    auto load = [&](int j, int slot) {
+        int h0;
+        const RopeStretch<E> v = pick(place(j, h0));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (head[k] < heads && h0 + head[k] < v.H)
+                cp_async16(ring + slot * 64 + lane + 32 * k, v.src + (h0 + head[k]) * v.src_head + entry[k], 16);
+    };
+#pragma unroll 1
+    for (int k = 0; k < stages && k < mine; ++k) {
+        load(k, k);
+        cp_async_commit();
+    }
+    if (!ready()) {
+        cp_async_wait_all();
+        return false;
+    }
+    const float per_half = 1.0f / (float)half;
+    int slot = 0;
+#pragma unroll 1
+    for (int j = 0; j < mine; ++j) {
+        const int left = mine - j;  // as in rope_stream
+        if (left >= kRopeStages)
+            cp_async_wait_pending<kRopeStages - 1>();
+        else if (left >= kRopeStages / 2)
+            cp_async_wait_pending<kRopeStages / 2 - 1>();
+        else
+            cp_async_wait_pending<0>();
+        __syncwarp();
+        int h0;
+        const int which = place(j, h0);
+        const RopeStretch<E> v = pick(which);
+        if (which < turned) {
+            const int pairs = min(heads, v.H - h0) * half;
+            E *at = reinterpret_cast<E *>(ring + slot * 64);
+            for (int i = lane; i < pairs; i += 32) {
+                const int h = (int)(((float)i + 0.5f) * per_half), k = i - h * half;  // i < 2^8: exact
+                E *a = at + h * pieces * W + (HALF ? k : 2 * k), *b = a + (HALF ? half : 1);
+                const float u = to_f32(*a), w = to_f32(*b), c = cs[k], s = cs[half + k];
+                from_f32(__fmaf_rn(u, c, -__fmul_rn(w, s)), *a);
+                from_f32(__fmaf_rn(w, c, __fmul_rn(u, s)), *b);
+            }
+            __syncwarp();
+        }
+        E *to = dst(which);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (head[k] < heads && h0 + head[k] < v.H)
+                *reinterpret_cast<uint4 *>(to + (h0 + head[k]) * v.dst_head + entry[k]) = ring[slot * 64 + lane + 32 * k];
+        if (j + stages < mine) {
+            load(j + stages, slot);
+            cp_async_commit();
+        }
+        slot = slot + 1 == stages ? 0 : slot + 1;
+    }
+    return true;
+}
+
 // The warp's token's R/2 cosines, then R/2 sines, into cs.
 __device__ __forceinline__ void rope_angles(float *cs, const double *inv_freq, int half, int32_t pos, float scale, bool inverse)
 {
@@ -446,79 +549,27 @@ __global__ void __launch_bounds__(kRopeThreads, !STREAM && sizeof(Piece<E, W>) =
             share, shares, [] { return true; }, [&] { return reinterpret_cast<uint8_t *>(y + p.R); });
 }
 
-// Heads of 16-byte pieces whose R/2 is not a multiple of a piece's entries: the pieces are streamed as they lie, 64 / pieces
-// heads to a step, and the pairs turned in shared memory one by one, across the lanes, before the pieces go out.
-// (8284 tokens of 19 heads of 192 bf16 with 74 entries turned: 25.9 us, 46.5 when lanes read and wrote single entries; 9000
-// of 2 heads of 256, 254 turned: 9.9 and 17.5; 32 heads of 80, 20 turned: one token 2.4 and 2.9, 2048 6.7 and 6.1.)
+// rope_kernel with the staged walk.
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_staged_kernel(const RopeParams p, int shares, int stages)
 {
-    constexpr int W = 16 / (int)sizeof(E);
     extern __shared__ __align__(16) uint8_t rope_smem[];  // as in rope_kernel
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.R / 2;
+    const int warp = threadIdx.x >> 5;
     uint4 *ring = reinterpret_cast<uint4 *>(rope_smem) + warp * stages * 64;
     float *cs = reinterpret_cast<float *>(rope_smem + kRopeWarps * stages * 1024) + warp * p.R;
     const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp, t = gw / shares;
     griddep_wait();
     griddep_launch_dependents();
     if (t >= p.T) return;
-    const int share = (int)(gw - t * shares), heads = 64 / p.pieces, steps = (p.H + heads - 1) / heads;
-    if (share >= steps) return;
-    const int mine = (steps - share + shares - 1) / shares;
-    const E *x = static_cast<const E *>(p.x) + t * p.x_token;
     E *y = static_cast<E *>(p.y) + t * p.y_token;
-    int head[2], entry[2];  // of this lane's two pieces in a step
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int i = lane + 32 * k;
-        head[k] = i / p.pieces;
-        entry[k] = (i - head[k] * p.pieces) * W;
-        if (head[k] >= heads) head[k] = p.H;  // none
-    }
-    auto load = [&](int j, int slot) {
-        const int h0 = (share + j * shares) * heads;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (h0 + head[k] < p.H) cp_async16(ring + slot * 64 + lane + 32 * k, x + (h0 + head[k]) * p.x_head + entry[k], 16);
-    };
-#pragma unroll 1
-    for (int k = 0; k < stages && k < mine; ++k) {
-        load(k, k);
-        cp_async_commit();
-    }
-    rope_angles(cs, p.inv_freq, half, p.pos[t], p.scale, p.inverse != 0);
-    const float per_half = 1.0f / (float)half;
-    int slot = 0;
-#pragma unroll 1
-    for (int j = 0; j < mine; ++j) {
-        const int left = mine - j;  // as in rope_stream
-        if (left >= kRopeStages)
-            cp_async_wait_pending<kRopeStages - 1>();
-        else if (left >= kRopeStages / 2)
-            cp_async_wait_pending<kRopeStages / 2 - 1>();
-        else
-            cp_async_wait_pending<0>();
-        __syncwarp();
-        const int h0 = (share + j * shares) * heads, pairs = min(heads, p.H - h0) * half;
-        E *at = reinterpret_cast<E *>(ring + slot * 64);
-        for (int i = lane; i < pairs; i += 32) {
-            const int h = (int)(((float)i + 0.5f) * per_half), k = i - h * half;  // i < 2^8: exact
-            E *a = at + h * p.pieces * W + (HALF ? k : 2 * k), *b = a + (HALF ? half : 1);
-            const float u = to_f32(*a), v = to_f32(*b), c = cs[k], s = cs[half + k];
-            from_f32(__fmaf_rn(u, c, -__fmul_rn(v, s)), *a);
-            from_f32(__fmaf_rn(v, c, __fmul_rn(u, s)), *b);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (h0 + head[k] < p.H)
-                *reinterpret_cast<uint4 *>(y + (h0 + head[k]) * p.y_head + entry[k]) = ring[slot * 64 + lane + 32 * k];
-        if (j + stages < mine) {
-            load(j + stages, slot);
-            cp_async_commit();
-        }
-        slot = slot + 1 == stages ? 0 : slot + 1;
-    }
+    const RopeStretch<E> st[1] = {{static_cast<const E *>(p.x) + t * p.x_token, p.x_head, p.y_head, p.H}};
+    rope_staged<E, HALF>(
+        st, 1, p.R, p.pieces, (int)(gw - t * shares), shares, ring, stages, cs,
+        [&] {
+            rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
+            return true;
+        },
+        [&](int) { return y; });
 }
 
 // ------------------------------------------------------------------------------- paged append
@@ -553,6 +604,7 @@ struct AppendParams {
     const double *inv_freq;    // null when R = 0
     int64_t T, pages;
     int32_t B, Hq, Hkv, D, R, page_size, max_pages;
+    int32_t pieces;               // rope_staged: 16-byte pieces of a head
     int32_t rest_piece, v_piece;  // bytes per copied piece of entries R .. D-1 of queries and keys (0: none), and of values
     float scale;
     int32_t *status;
@@ -594,8 +646,9 @@ __host__ __device__ inline bool append_values(const AppendParams &p)
 }
 
 // `shares` warps take a token's query heads, key heads and values in turn.
-template <int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel(const AppendParams p, int shares, int stages)
+template <int W, bool HALF, bool STAGED = false>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+    paged_append_kernel(const AppendParams p, int shares, int stages)
 {
     using E = __nv_bfloat16;
     extern __shared__ __align__(16) uint8_t rope_smem[];  // as in rope_kernel
@@ -627,6 +680,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) paged_append_kernel
     E *qo = p.q_out + t * p.qo_token;
     auto bytes_at = [](E *e) { return reinterpret_cast<uint8_t *>(e); };
     constexpr int kE = sizeof(E);
+    if constexpr (STAGED) {
+        const RopeStretch<E> st[3] = {{q, p.q_head, p.qo_head, p.q != nullptr ? p.Hq : 0},
+                                      {k, p.k_head, p.c_head, p.Hkv},
+                                      {v, p.v_head, p.c_head, p.Hkv}};
+        rope_staged<E, HALF>(st, 2, p.R, p.pieces, share, shares, ring, stages, cs, ready,
+                             [&](int i) { return i == 0 ? qo : (i == 1 ? p.k_cache : p.v_cache) + row; });
+        return;
+    }
     int rest = p.rest_piece ? p.D - p.R : 0;  // entries left to copy after the walk
     if constexpr (W == 8) {
         const RopeStretch<E> st[3] = {{q, p.q_head, p.qo_head, p.q != nullptr ? p.Hq : 0},

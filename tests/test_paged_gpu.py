@@ -508,3 +508,26 @@ def test_append_long_prompts_take_one_warp_per_token(Hq, Hkv, D, R, layout):
     if Hq:
         assert same_bits(q_out[t], turned(q)) and bool((q_out[2600:] == 7.0).all())
     assert bi.bi_get_device_status() == bi.BI_OK
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("Hq,Hkv,D,R", [(32, 32, 80, 20), (0, 5, 192, 74), (4, 2, 512, 510), (7, 1, 24, 22)])
+def test_append_pairs_that_fill_no_pieces(Hq, Hkv, D, R, layout):
+    test_append_long_prompts_take_one_warp_per_token(Hq, Hkv, D, R, layout)
+    g = gen(D)  # a few tokens, values and then keys without 16-byte alignment: other walks, the same bits
+    lens, page, T = [5, 0, 33, 128], 16, 4
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(T, Hkv, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    f = bi.bi_rope_freqs(R, 1e4)[0]
+    kc, vc = make_cache(g, 14, page, Hkv, D)
+    table = make_table(g, lens, page, 14)
+    odd = []
+    for x in (k, v):
+        odd.append(torch.empty(T * Hkv * D + 1, dtype=torch.bfloat16, device=DEV)[1:].view(T, Hkv, D))
+        odd[-1].copy_(x)
+    want = None
+    for a, b in ((k, v), (k, odd[1]), (odd[0], v)):
+        k2, v2 = kc.clone(), vc.clone()
+        bi.bi_paged_append(a, b, k2, v2, table, sl, None, f, layout)
+        want = want or (k2, v2)
+        assert same_bits(k2, want[0]) and same_bits(v2, want[1])
