@@ -12,9 +12,9 @@
 //
 // Bound by the cache's bytes (B200: 64 sequences of 4096 tokens, 32 / 8 heads of 128, pages of 16, 170 us or
 // 6.3 TB/s; 256 of 512 tokens 81.7 us, 6.6 TB/s) and, for a few short sequences, by latency: prefix sums, page
-// table and first tile take about 2 us, a tile 0.7 us, the fold 0.7 us.  One persistent CTA per SM; the (split, kv head) items of the batch are
-// numbered through the prefix sums of the sequences' split counts, so a CTA's share does not depend on
-// how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
+// table and first tile take about 2 us, a tile 0.7 us, the fold 0.7 us.  One persistent CTA per SM; the (split, kv
+// head) items of the batch are numbered through the prefix sums of the sequences' split counts, so a CTA's share does not
+// depend on how ragged the batch is; two consumer groups take alternate items, so that one's folding overlaps the
 // other's arithmetic and loads.  The producers fill a ring of tiles (K and V of 32 tokens: 16 KB at
 // head size 128, 8 tiles; 8 KB at 64, 20 tiles) by TMA: boxes of gcd(P, kPgTile) tokens x 64
 // entries, each within one page and completing on the tile's mbarrier.  The lanes look pages up one chunk of
