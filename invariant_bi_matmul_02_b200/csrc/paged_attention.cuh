@@ -23,9 +23,9 @@
 //
 // Tensor-core work (mma.sync m16n8k16, bf16 in, fp32 accumulate): S^T = K Q^T with tokens on the 16
 // rows and the group's heads on the 8 columns (two column tiles for groups of 9 to 16), then
-// O^T += V^T P^T with the head's entries on the rows.  The weights P enter as two bf16 terms (hi =
-// bf16(p), lo = bf16(p - hi), about 16 significant bits), so the only rounding to 8 bits is the
-// output's.
+// O^T += V^T P^T with the head's entries on the rows.  An fp32 weight enters as three bf16 terms, its upper 8, next 8
+// and last 8 bits (pg_terms), whose sum it is, so the only rounding to fewer than 24 bits is the output's.  (With two
+// terms, 16 bits, one output in 500 rounded the other way.)
 #pragma once
 
 #include <cstdint>
@@ -111,6 +111,19 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// Weights x and y as bf16 terms, each the upper half of what is left of its fp32 word (x low, y high in a register),
+// turned so that tokens run along a thread's registers.  Every difference is exact; terms below 2^-133 are lost.
+__device__ __forceinline__ void pg_terms(uint32_t (&t)[3], float x, float y)
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+        t[i] = movm_trans(__byte_perm(a, b, 0x7632));
+        x = __fsub_rn(x, __uint_as_float(a & 0xffff0000u));
+        y = __fsub_rn(y, __uint_as_float(b & 0xffff0000u));
+    }
 }
 
 // Launch 1: grid = min(items, SMs).  Item i: kv head i % Hkv of the global split i / Hkv (kv head
@@ -368,7 +381,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         }
                     }
                     // ---- running maximum, rescaled sums, weights; tokens past the sequence weigh nothing
-                    uint32_t hi[NT][2][2], lo[NT][2][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
@@ -407,21 +419,15 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) o[nt][mt][e] = __fmul_rn(o[nt][mt][e], f[e & 1]);
                         }
-                        // Weights as two bf16 terms, turned so that tokens run along a thread's registers.
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float x = s[nt][mt][2 * r], y = s[nt][mt][2 * r + 1];
-                                const float xh = __bfloat162float(__float2bfloat16_rn(x));
-                                const float yh = __bfloat162float(__float2bfloat16_rn(y));
-                                hi[nt][mt][r] = movm_trans(pack_bf16(xh, yh));
-                                lo[nt][mt][r] = movm_trans(pack_bf16(x - xh, y - yh));
-                            }
                     }
-                    // ---- O^T += V^T P^T over two 16-token steps in ascending order, hi before lo
+                    // ---- O^T += V^T P^T over two 16-token steps in ascending order, the larger terms first
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
+                        uint32_t w[NT][2][3];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) pg_terms(w[nt][r], s[nt][mt][2 * r], s[nt][mt][2 * r + 1]);
                         // Value rows past the sequence hold anything: their bits are cleared.
                         const int ta = 16 * mt + 2 * tig;
                         uint32_t keep[2];
@@ -434,10 +440,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                             ldsm_x4_trans(v, chunk(vs, 16 * mt + (lane & 15), dt + (lane >> 4)));
                             const uint32_t a[4] = {v[0] & keep[0], v[2] & keep[0], v[1] & keep[1], v[3] & keep[1]};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma_16816_bf16(o[nt][dt / 2], a, hi[nt][mt][0], hi[nt][mt][1]);
-                                mma_16816_bf16(o[nt][dt / 2], a, lo[nt][mt][0], lo[nt][mt][1]);
-                            }
+                            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_16816_bf16(o[nt][dt / 2], a, w[nt][0][i], w[nt][1][i]);
                         }
                     }
                     __syncwarp();

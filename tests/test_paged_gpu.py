@@ -531,3 +531,26 @@ def test_append_pairs_that_fill_no_pieces(Hq, Hkv, D, R, layout):
         bi.bi_paged_append(a, b, k2, v2, table, sl, None, f, layout)
         want = want or (k2, v2)
         assert same_bits(k2, want[0]) and same_bits(v2, want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [8, 16])
+def test_attention_weights_keep_their_24_bits(G, D):
+    """Three tokens of weights 1, 1 and p in (1/2, 1), whose values -hi, -mid and 1 (hi = bf16(p), mid = bf16(p - hi)) leave
+    p's last bits.  In units of 2^-24: p is off by at most 4 (score's scaling and rounding 1.4, ex2 2), the sums of a dozen
+    terms below 1 by 24; over the sum of the weights, 2 + p, and with one rounding of a value below 2^-17."""
+    B = 64
+    s = (0.69 * torch.rand(B, G, generator=gen(17), device=DEV)).to(torch.bfloat16)
+    p = torch.exp(-s.double())
+    hi = p.float().to(torch.bfloat16)
+    mid = (p - hi.double()).float().to(torch.bfloat16)
+    kc, vc = (torch.zeros(B, 4, 1, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    kc[:, 2, 0, 0] = -1.0
+    vc[:, 0, 0, :G], vc[:, 1, 0, :G], vc[:, 2, 0, :G] = -hi, -mid, 1.0  # entry h for head h
+    q = torch.zeros(B, G, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = s
+    table = torch.arange(B, dtype=torch.int32, device=DEV).view(B, 1)
+    o = bi.bi_paged_decode_attention(q, kc, vc, table, torch.full((B,), 3, dtype=torch.int32, device=DEV), scale=1.0)
+    got = torch.diagonal(o[..., :G].double(), dim1=1, dim2=2)
+    want = (p - hi.double() - mid.double()) / (2 + p)
+    close(got, want, 28 * 2.0 ** -24 / (2 + p) + 2.0 ** -8 * want.abs())
