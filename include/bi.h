@@ -308,7 +308,8 @@ size_t bi_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64
  *              heads token_stride / head_stride elements apart (any strides >= 0 for x; those of y
  *              must keep its heads apart).  y may be x itself with the same strides.
  *   positions  device, int32, [T], any sign.
- *   inv_freq   device, fp64, [R/2] (bi_rope_freqs).  R even, 0 <= R <= D <= 1024.
+ *   inv_freq   device, fp64, [R/2] (bi_rope_freqs).  R even, 0 <= R <= D <= 1024.  R = 0: nothing is turned, and positions
+ *              and inv_freq may be NULL.
  *   layout     BI_ROPE_HALF: pair i is entries (i, i + R/2); BI_ROPE_INTERLEAVED: (2i, 2i + 1).
  *   The angle is an fp64 product reduced to a fraction of a turn, so far positions keep their
  *   digits; the rest is fp32 with one rounding to bf16.  16-byte pieces are moved where R/2, D - R,

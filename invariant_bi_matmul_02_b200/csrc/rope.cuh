@@ -501,7 +501,7 @@ struct RopeParams {
     const void *x;
     void *y;
     int64_t x_token, x_head, y_token, y_head;  // strides in entries
-    const int32_t *pos;
+    const int32_t *pos;  // pos and inv_freq may be null when R = 0
     const double *inv_freq;
     int64_t T;
     int32_t H, D, R;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kRopeThreads, !STREAM && sizeof(Piece<E, W>) =
     E *y = static_cast<E *>(p.y) + t * p.y_token;
     bool have = false;
     auto ready = [&] {
-        if (!have) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
+        if (!have && p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, p.pos[t], p.scale, p.inverse != 0);
         have = true;
         return true;
     };

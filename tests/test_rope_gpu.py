@@ -143,6 +143,19 @@ def test_rope_empty_calls_streams_and_graphs():
     assert same_bits(out, want2)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D", [(1, 1, 1), (5, 3, 64), (7, 2, 10), (2400, 7, 80), (2401, 3, 9)])
+def test_rope_nothing_turned_needs_no_positions(T, H, D, dtype):
+    """R = 0 through the C entry with positions and inv_freq NULL: a copy, streamed or not."""
+    x, _, _ = make(37, T, H, D, 0, dtype)
+    y = torch.full_like(x, 7.0)
+    s = torch.cuda.current_stream().cuda_stream
+    for out in (y, x):  # in place nothing moves
+        assert bi.load().bi_rope(x.data_ptr(), H * D, D, out.data_ptr(), H * D, D, bi._DT[dtype], None, None, T, H, D, 0, 0,
+                                 1.0, 0, s) == bi.BI_OK
+        assert same_bits(y, x)
+
+
 def test_rope_binding_refusals():
     x, pos, f = make(31, 4, 2, 8, 8, torch.bfloat16)
     for bad in (lambda: bi.bi_rope(x.half(), pos, f), lambda: bi.bi_rope(x, pos.long(), f),
