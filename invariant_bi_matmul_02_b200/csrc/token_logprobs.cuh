@@ -192,6 +192,17 @@ struct TlGroup {
         for (int i = 1; i < kTlWords; ++i) m = fmaxf(m, __uint_as_float(w[i]));
         return m;
     }
+    // The maximum of the first n elements (1 .. kSize); NaN where no number is among them.
+    __device__ __forceinline__ float max_below(int n) const
+    {
+        float m = __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int i = 0; i < kSize; ++i) {
+            const uint32_t bits = !BF16 ? w[i] : i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16;
+            if (i < n) m = fmaxf(m, __uint_as_float(bits));
+        }
+        return m;
+    }
     // Sums of e = 2^((x - ref) c) and of e (x - ref) c over the group, in two interleaved chains.  A logit of
     // -inf has e = 0 and would make 0 * -inf: CLAMP keeps the factor finite (below -1000 e is 0 already).
     template <bool CLAMP>
@@ -464,12 +475,19 @@ __global__ void __launch_bounds__(kTlThreads, kTlBlocks) token_logprobs_kernel(c
     for (int piece = rank; piece < p.pieces; piece += p.cluster, ++local) {
         const int ahead = piece + p.cluster;
         if (ahead < p.pieces) next.template load<VEC>(row, ahead * kPiece + kGroup * tid, p.V);
-        const float gm = g.max();
+        const float gm = g.max(), m = warp_max(gm);
         if (p.top > 0) {
             tl_max[local * kTlThreads + tid] = tl_keep(gm);
-            if (piece * kPiece + kGroup * tid < p.V) thread_best = fmaxf(thread_best, gm);
+            if (ahead < p.pieces) {
+                thread_best = fmaxf(thread_best, gm);
+            } else {
+                // The row may end here.  The -inf past its end are no elements: a group that it cuts and that holds NaN
+                // only does not reach -inf.
+                const int left = p.V - (piece * kPiece + kGroup * tid);
+                const float own = gm == kNegInf && left < kGroup && left > 0 ? g.max_below(left) : gm;
+                if (left > 0) thread_best = fmaxf(thread_best, own);
+            }
         }
-        const float m = warp_max(gm);
         const float ref = m == kNegInf ? 0.0f : m;
         float s, t;
         if (!masked) {

@@ -8,6 +8,7 @@ Tolerances, with u = 2^-24, d_j = scale (x_j - max x), p the probabilities, E1 =
 * T = sum e d: each d is off by 3 u |d| on top of e's error, same chain: T / S by u (190 E1 + 6 E2) + s_err E1;
   entropy = log S - T / S: that plus s_err + 2 u (E1 + |entropy|).
 """
+import ctypes
 import math
 
 import pytest
@@ -244,3 +245,39 @@ def test_few_tokens_clear_of_a_mask(M, V, kept, low, dtype):
     y.scatter_(1, at, x.gather(1, at).abs() + 1)
     check(y, at[:, 0].to(torch.int32), 0.9, 8)
     check(y, at[:, 0].to(torch.int32), 0.9, 32)
+
+
+def nan_last(row, k):
+    """The k best tokens of a row: numbers in descending order, then NaN, equals by ascending token."""
+    by = torch.sort(torch.where(row.isnan(), -math.inf, row.double()), descending=True, stable=True)[1]
+    return by[torch.sort(row.isnan()[by].int(), stable=True)[1]][:k]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [2, 40, 1000, 1024, 9000, 50257])
+@pytest.mark.parametrize("M", [9, 711])
+def test_every_place_of_the_best_is_written_in_rows_of_nan(M, V, dtype):
+    """Rows with fewer numbers than top_k, and their last group of elements cut by the row's end, at one block a row and
+    at more: every place holds a token, numbers first."""
+    nan, inf = math.nan, math.inf
+    kinds = torch.full((9, V), nan, dtype=dtype)
+    kinds[1, 0] = 1.0
+    kinds[2, V - 1] = 1.0
+    kinds[3, V // 2] = -inf
+    kinds[4, :V - 1] = -inf
+    kinds[5, :V // 2] = -2.0
+    kinds[6, :V - 1] = 3.0
+    kinds[7, ::7] = 0.5
+    kinds[8, 0], kinds[8, V - 1] = -inf, -inf if V > 2 else nan
+    x = kinds.to(DEV).repeat(-(-M // 9), 1)[:M].contiguous()
+    for k in (1, 2, 5, 32):
+        if k > V:
+            continue
+        tl = torch.full((M, k), 77.0, device=DEV)
+        tt = torch.full((M, k), -12345, dtype=torch.int32, device=DEV)
+        stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert bi.load().bi_token_logprobs(x.data_ptr(), V, bi._DT[dtype], None, 1.0, k, None, None, None, tl.data_ptr(),
+                                           tt.data_ptr(), M, V, stream) == bi.BI_OK
+        want = torch.stack([nan_last(r, k) for r in x[:9]])
+        assert torch.equal(tt.long(), want.repeat(-(-M // 9), 1)[:M]), k
+        assert bool(tl.isnan().all()), k
