@@ -4,14 +4,14 @@
 // thirty arguments in Python costs several times the kernel (17 us for bi_paged_append, whose kernel
 // takes 4).  The module does what binding.py's other functions do in Python, and nothing else: it
 // checks device, dtype and layout of the torch tensors, allocates outputs with torch when none are
-// passed, and calls the C entry point with raw device pointers, strides and the current stream.  The entry
+// passed, from the pool of the call's stream, and calls the C entry point with raw device pointers and strides.  The entry
 // points' addresses come from the library that binding.py has loaded (bind).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -108,14 +108,23 @@ int64_t integer(PyObject *o)
     return v;
 }
 
-// binding.py passes a raw stream handle, or None for torch's current stream.
-void *stream_of(PyObject *o, int dev)
-{
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    void *s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw python_error();
-    return s;
-}
+// The call's stream: binding.py passes a raw handle, or None for torch's current stream.  A handle's stream is torch's
+// current one while this lives, so that memory made for the call is that stream's: a block whose last work on another
+// stream is still to run is not handed out, and one that is freed early is not reused before the call's own work.
+struct CallStream {
+    void *raw;
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    CallStream(PyObject *o, int dev)
+    {
+        if (o == Py_None) {
+            raw = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+            return;
+        }
+        raw = PyLong_AsVoidPtr(o);
+        if (!raw && PyErr_Occurred()) throw python_error();
+        guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), (c10::DeviceIndex)dev));
+    }
+};
 
 void *ptr(const Tensor &t) { return t.data_ptr(); }
 
@@ -171,16 +180,16 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t T = x.size(0), H = x.size(1), D = x.size(2);
     const Tensor &pos = vec(a[1], "positions", at::kInt, T, dev), &freq = vec(a[2], "inv_freq", at::kDouble, -1, dev);
     const bi_rope_layout layout = rope_layout(a[3]);
+    const CallStream stream(a[7], dev);
     Out out{a[6], {}};
     if (out.given == Py_None) out.made = empty({T, H, D}, x.scalar_type(), dev);
     const Tensor &y = out.given == Py_None ? out.made : heads(out.given, "out", x.scalar_type(), x.scalar_type(), dev);
     if (y.sizes() != x.sizes()) value_error("out must be [T, H, D]");
     const float scale = (float)number(a[4]);
     const int inverse = PyObject_IsTrue(a[5]);
-    void *s = stream_of(a[7], dev);
     BI_CALL("bi_rope", p_rope, ptr(x), x.stride(0), x.stride(1), ptr(y), y.stride(0), y.stride(1),
             x.scalar_type() == at::kBFloat16 ? BI_BF16 : BI_F32, static_cast<const int32_t *>(ptr(pos)),
-            static_cast<const double *>(ptr(freq)), T, H, D, 2 * freq.size(0), layout, scale, inverse, s)
+            static_cast<const double *>(ptr(freq)), T, H, D, 2 * freq.size(0), layout, scale, inverse, stream.raw)
     return out.result();
     END_HANDLE_TH_ERRORS
 }
@@ -235,6 +244,7 @@ PyObject *paged_append(PyObject *, PyObject *const *a, Py_ssize_t n)
     const bi_rope_layout layout = rope_layout(a[8]);
     const float scale = (float)number(a[9]);
     const void *pos = a[12] == Py_None ? nullptr : ptr(vec(a[12], "positions", at::kInt, T, dev));
+    const CallStream stream(a[13], dev);
     Out out{a[11], {}};
     const Tensor *q = nullptr, *qo = nullptr;
     if (a[10] != Py_None) {
@@ -248,13 +258,12 @@ PyObject *paged_append(PyObject *, PyObject *const *a, Py_ssize_t n)
     }
     const int64_t Hq = q ? q->size(1) : 0;
     const bool turn = Hq > 0;
-    void *s = stream_of(a[13], dev);
     BI_CALL("bi_paged_append", p_paged_append, ptr(k), k.stride(0), k.stride(1), ptr(v), v.stride(0), v.stride(1),
             turn ? ptr(*q) : nullptr, turn ? q->stride(0) : 0, turn ? q->stride(1) : 0, turn ? ptr(*qo) : nullptr,
             turn ? qo->stride(0) : 0, turn ? qo->stride(1) : 0, Hq, &cache, static_cast<const int32_t *>(ptr(table)),
             table_stride, table.size(1), static_cast<const int32_t *>(ptr(lens)), static_cast<const int32_t *>(cu),
             static_cast<const int32_t *>(pos), freq ? static_cast<const double *>(ptr(*freq)) : nullptr,
-            freq ? 2 * freq->size(0) : 0, layout, scale, T, B, s)
+            freq ? 2 * freq->size(0) : 0, layout, scale, T, B, stream.raw)
     if (!q) Py_RETURN_NONE;
     return out.result();
     END_HANDLE_TH_ERRORS
@@ -276,6 +285,7 @@ PyObject *paged_decode_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t table_stride = leading(table, "block_table"), max_pages = table.size(1);
     const int64_t max_len = a[5] == Py_None ? max_pages * cache.page_size : integer(a[5]);
     const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)number(a[6]);
+    const CallStream stream(a[9], dev);
     Out out{a[8], {}};
     if (out.given == Py_None) out.made = empty(q.sizes(), bf16, dev);
     const Tensor &o = out.given == Py_None ? out.made : cuda_tensor(out.given, "out", bf16, bf16, dev);
@@ -290,15 +300,9 @@ PyObject *paged_decode_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         scratch = &cuda_tensor(a[7], "scratch", THPVariable_Unpack(a[7]).scalar_type(), THPVariable_Unpack(a[7]).scalar_type(), dev);
         if (!scratch->is_contiguous()) value_error("scratch must be contiguous");
     }
-    void *s = stream_of(a[9], dev);
-    // Scratch made here is freed when this returns, for reuse on torch's current stream: work on another stream
-    // is made known to the allocator.
-    if (own.defined() && a[9] != Py_None)
-        c10::cuda::CUDACachingAllocator::recordStream(
-            own.storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), (c10::DeviceIndex)dev));
     BI_CALL("bi_paged_decode_attention", p_paged_decode_attention, ptr(q), q.stride(0), &cache,
             static_cast<const int32_t *>(ptr(table)), table_stride, max_pages, static_cast<const int32_t *>(ptr(lens)),
-            ptr(o), B, Hq, max_len, scale, ptr(*scratch), scratch->nbytes(), s)
+            ptr(o), B, Hq, max_len, scale, ptr(*scratch), scratch->nbytes(), stream.raw)
     return out.result();
     END_HANDLE_TH_ERRORS
 }
@@ -315,6 +319,7 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
     const bool scored = a[1] != Py_None;
     const void *tok = scored ? ptr(vec(a[1], "tokens", at::kInt, M, dev)) : nullptr;
     const float scale = (float)number(a[3]);
+    const CallStream stream(a[4], dev);
     // One allocation holds the five results (each M or M * top four-byte values, a multiple of 16 bytes apart).
     auto room = [](int64_t values) { return (values + 3) / 4 * 4; };
     const Tensor buffer = empty({3 * room(M) + 2 * room(M * top)}, at::kFloat, dev);
@@ -329,11 +334,10 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
     };
     const Tensor lp = part({M}, at::kFloat), h = part({M}, at::kFloat), lse = part({M}, at::kFloat),
                  tl = part({M, top}, at::kFloat), tt = part({M, top}, at::kInt);
-    void *s = stream_of(a[4], dev);
     BI_CALL("bi_token_logprobs", p_token_logprobs, ptr(x), ld, x.scalar_type() == at::kBFloat16 ? BI_BF16 : BI_F32,
             static_cast<const int32_t *>(tok), scale, top, scored ? static_cast<float *>(ptr(lp)) : nullptr,
             static_cast<float *>(ptr(h)), static_cast<float *>(ptr(lse)), static_cast<float *>(ptr(tl)),
-            static_cast<int32_t *>(ptr(tt)), M, V, s)
+            static_cast<int32_t *>(ptr(tt)), M, V, stream.raw)
     PyObject *r = PyTuple_New(5);
     if (!r) return nullptr;
     if (!scored) Py_INCREF(Py_None);
