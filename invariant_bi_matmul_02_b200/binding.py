@@ -1,9 +1,10 @@
 """Python binding of libbi.so: the C ABI of include/bi.h, one function per entry point.
 
 Argument marshalling only.  Each function checks device, dtype and layout of the
-torch tensors it is given, allocates the output with torch when none is passed,
-and calls the C entry point of the same name with raw device pointers, leading
-dimensions and the current CUDA stream.  The operators of a decode step (rotation, paged
+torch tensors it is given, allocates the output with torch when none is passed (a
+call on a given stream from that stream's pool, as under torch.cuda.stream), and
+calls the C entry point of the same name with raw device pointers, leading
+dimensions and the CUDA stream (default: the current one).  The operators of a decode step (rotation, paged
 cache, token log-probabilities) do this in the extension module _marshal, whose calls
 cost a fraction of the Python checks.  Every step of the computation runs in
 libbi.so's kernels; there is no fallback.  If libbi.so is missing or a call fails
@@ -166,6 +167,19 @@ def _ld(t: torch.Tensor, name: str) -> int:
     return s0 if rows > 1 else max(s0, cols)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory made for a call: from the pool of the call's stream, as under torch.cuda.stream, so that it is neither in
+    use by another stream's work nor reused before the call's own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        _same_device(stream.device.index, "stream")
+    else:
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _contig(t: torch.Tensor, name: str):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -194,7 +208,7 @@ def bi_matmul(a: torch.Tensor, b: torch.Tensor, b_layout: str = "nk", out: torch
     _need_cuda(b, "B", (torch.bfloat16,), cur)
     M, N, K = _gemm_shapes(a, b, b_layout)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _empty((M, N), out_dtype, a.device, stream)
     _need_cuda(out, "C", (torch.bfloat16, torch.float32), cur)
     if tuple(out.shape) != (M, N):
         raise ValueError("C must be [M, N]")
@@ -224,7 +238,7 @@ def bi_addmm(input: torch.Tensor, a: torch.Tensor, b: torch.Tensor, b_layout: st
             raise ValueError("input must be [N] or [M, N]")
         ld_in = _ld(input, "input")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _empty((M, N), out_dtype, a.device, stream)
     _need_cuda(out, "C", (torch.bfloat16, torch.float32), cur)
     if tuple(out.shape) != (M, N):
         raise ValueError("C must be [M, N]")
@@ -246,7 +260,7 @@ def bi_matmul_silu_mul(a: torch.Tensor, b: torch.Tensor, b_layout: str = "nk",
         raise ValueError("B must stack gate and up: an even number of output rows")
     F = N2 // 2
     if out is None:
-        out = torch.empty((M, F), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M, F), torch.bfloat16, a.device, stream)
     _need_cuda(out, "H", (torch.bfloat16,), cur)
     if tuple(out.shape) != (M, F):
         raise ValueError("H must be [M, F]")
@@ -268,7 +282,7 @@ def bi_rmsnorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, out: torch.T
     if tuple(w.shape) != (H,):
         raise ValueError("w must be [H]")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     _need_cuda(out, "y", (torch.bfloat16,))
     _contig(out, "y")
     _check("bi_rmsnorm", load().bi_rmsnorm(x.data_ptr(), w.data_ptr(), out.data_ptr(), M, H,
@@ -282,7 +296,7 @@ def bi_mean(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> to
     _contig(x, "x")
     M, H = x.shape
     if out is None:
-        out = torch.empty((M,), dtype=torch.float32, device=x.device)
+        out = _empty((M,), torch.float32, x.device, stream)
     _need_cuda(out, "y", (torch.float32,))
     _contig(out, "y")
     _check("bi_mean", load().bi_mean(x.data_ptr(), out.data_ptr(), M, H, _stream(stream)))
@@ -295,7 +309,7 @@ def bi_log_softmax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None
     _contig(x, "x")
     M, V = x.shape
     if out is None:
-        out = torch.empty((M, V), dtype=torch.float32, device=x.device)
+        out = _empty((M, V), torch.float32, x.device, stream)
     _need_cuda(out, "y", (torch.float32,))
     _contig(out, "y")
     _check("bi_log_softmax", load().bi_log_softmax(x.data_ptr(), _DT[x.dtype], out.data_ptr(), M, V,
@@ -310,7 +324,7 @@ def bi_log_softmax_cluster(x: torch.Tensor, out: torch.Tensor | None = None, str
     _contig(x, "x")
     M, V = x.shape
     if out is None:
-        out = torch.empty((M, V), dtype=torch.float32, device=x.device)
+        out = _empty((M, V), torch.float32, x.device, stream)
     _need_cuda(out, "y", (torch.float32,))
     _contig(out, "y")
     _check("bi_log_softmax_cluster", load().bi_log_softmax_cluster(x.data_ptr(), _DT[x.dtype], out.data_ptr(), M,
@@ -330,12 +344,12 @@ def bi_log_softmax_split(x: torch.Tensor, scratch: torch.Tensor | None = None,
     _contig(x, "x")
     M, V = x.shape
     if out is None:
-        out = torch.empty((M, V), dtype=torch.float32, device=x.device)
+        out = _empty((M, V), torch.float32, x.device, stream)
     _need_cuda(out, "y", (torch.float32,))
     _contig(out, "y")
     need = bi_log_softmax_split_scratch_bytes(M, V)
     if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        scratch = _empty((max(need, 16),), torch.uint8, x.device, stream)
     if not scratch.is_cuda:
         raise ValueError("scratch must be device memory")
     _same_device(scratch.get_device(), "scratch")
@@ -369,7 +383,7 @@ def bi_silu_mul(gu: torch.Tensor, out: torch.Tensor | None = None, stream=None) 
         raise ValueError("gu must have 2F columns")
     F = F2 // 2
     if out is None:
-        out = torch.empty((M, F), dtype=torch.bfloat16, device=gu.device)
+        out = _empty((M, F), torch.bfloat16, gu.device, stream)
     _need_cuda(out, "h", (torch.bfloat16,))
     _contig(out, "h")
     _check("bi_silu_mul", load().bi_silu_mul(gu.data_ptr(), out.data_ptr(), M, F, _stream(stream)))
@@ -397,14 +411,14 @@ def bi_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need_cuda(out, "out", (torch.bfloat16,))
     _contig(out, "out")
     if tuple(out.shape) != tuple(q.shape):
         raise ValueError("out must be [B, Hq, D]")
     if scratch is None:
-        scratch = torch.empty(max(bi_decode_attention_scratch_bytes(B, Hq, D, Lmax), 16), dtype=torch.uint8,
-                              device=q.device)
+        need = bi_decode_attention_scratch_bytes(B, Hq, D, Lmax)
+        scratch = _empty((max(need, 16),), torch.uint8, q.device, stream)
     if not scratch.is_cuda:
         raise ValueError("scratch must be device memory")
     _same_device(scratch.get_device(), "scratch")
