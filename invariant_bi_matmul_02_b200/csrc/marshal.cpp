@@ -320,20 +320,19 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
     const void *tok = scored ? ptr(vec(a[1], "tokens", at::kInt, M, dev)) : nullptr;
     const float scale = (float)number(a[3]);
     const CallStream stream(a[4], dev);
-    // One allocation holds the five results (each M or M * top four-byte values, a multiple of 16 bytes apart).
-    auto room = [](int64_t values) { return (values + 3) / 4 * 4; };
-    const Tensor buffer = empty({3 * room(M) + 2 * room(M * top)}, at::kFloat, dev);
-    int64_t at_value = 0;
-    auto part = [&](at::IntArrayRef sizes, at::ScalarType type) {
-        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(),
-                                                            c10::scalarTypeToTypeMeta(type));
+    // Each result has a storage of its own, so that one that is kept or saved takes none of the others along.  The later
+    // ones are made beside the dispatcher, as it makes the first (a one-row call 6.6 us on the host, 7.9 with five at::empty).
+    const Tensor h = empty({M}, at::kFloat, dev);
+    auto make = [&](at::IntArrayRef sizes, at::ScalarType type) {
+        const int64_t n = c10::multiply_integers(sizes);
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::Storage(c10::Storage::use_byte_size_t(), (size_t)n * 4, h.storage().allocator(), true), h.key_set(),
+            c10::scalarTypeToTypeMeta(type));
         t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-        t.unsafeGetTensorImpl()->set_storage_offset(at_value);
-        at_value += room(t.numel());
         return t;
     };
-    const Tensor lp = part({M}, at::kFloat), h = part({M}, at::kFloat), lse = part({M}, at::kFloat),
-                 tl = part({M, top}, at::kFloat), tt = part({M, top}, at::kInt);
+    const Tensor lp = scored ? make({M}, at::kFloat) : Tensor(), lse = make({M}, at::kFloat), tl = make({M, top}, at::kFloat),
+                 tt = make({M, top}, at::kInt);
     BI_CALL("bi_token_logprobs", p_token_logprobs, ptr(x), ld, x.scalar_type() == at::kBFloat16 ? BI_BF16 : BI_F32,
             static_cast<const int32_t *>(tok), scale, top, scored ? static_cast<float *>(ptr(lp)) : nullptr,
             static_cast<float *>(ptr(h)), static_cast<float *>(ptr(lse)), static_cast<float *>(ptr(tl)),

@@ -9,6 +9,7 @@ Tolerances, with u = 2^-24, d_j = scale (x_j - max x), p the probabilities, E1 =
   entropy = log S - T / S: that plus s_err + 2 u (E1 + |entropy|).
 """
 import ctypes
+import io
 import math
 
 import pytest
@@ -281,3 +282,15 @@ def test_every_place_of_the_best_is_written_in_rows_of_nan(M, V, dtype):
         want = torch.stack([nan_last(r, k) for r in x[:9]])
         assert torch.equal(tt.long(), want.repeat(-(-M // 9), 1)[:M]), k
         assert bool(tl.isnan().all()), k
+
+
+@pytest.mark.parametrize("k", [0, 4])
+def test_results_can_be_saved_and_kept_apart(k):
+    x, t = rows(13, 3, 500, torch.bfloat16)
+    r = bi.bi_token_logprobs(x, t, k)
+    at = io.BytesIO()
+    torch.save(tuple(r), at)
+    at.seek(0)
+    assert all(same_bits(a, b) for a, b in zip(torch.load(at), r))
+    assert all(v.untyped_storage().nbytes() == v.numel() * v.element_size() for v in r)
+    assert bi.bi_token_logprobs(x, None, k).logprobs is None
