@@ -108,6 +108,13 @@ int64_t integer(PyObject *o)
     return v;
 }
 
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v;
+}
+
 // The call's stream: binding.py passes a raw handle, or None for torch's current stream.  A handle's stream is torch's
 // current one while this lives, so that memory made for the call is that stream's: a block whose last work on another
 // stream is still to run is not handed out, and one that is freed early is not reused before the call's own work.
@@ -186,7 +193,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor &y = out.given == Py_None ? out.made : heads(out.given, "out", x.scalar_type(), x.scalar_type(), dev);
     if (y.sizes() != x.sizes()) value_error("out must be [T, H, D]");
     const float scale = (float)number(a[4]);
-    const int inverse = PyObject_IsTrue(a[5]);
+    const int inverse = truth(a[5]);
     BI_CALL("bi_rope", p_rope, ptr(x), x.stride(0), x.stride(1), ptr(y), y.stride(0), y.stride(1),
             x.scalar_type() == at::kBFloat16 ? BI_BF16 : BI_F32, static_cast<const int32_t *>(ptr(pos)),
             static_cast<const double *>(ptr(freq)), T, H, D, 2 * freq.size(0), layout, scale, inverse, stream.raw)

@@ -207,3 +207,14 @@ def test_rope_pairs_that_fill_no_pieces(T, H, D, R, dtype, layout):
     wide[..., :D] = x
     bi.bi_rope(wide[..., :D], pos, f, layout, 1.1, True, out=wide[..., :D])
     assert same_bits(wide[..., :D].contiguous(), y) and bool((wide[..., D:] == 3.0).all())
+
+
+def test_rope_inverse_without_a_truth_value():
+    """`inverse` that has no truth value raises its own error and turns nothing."""
+    x, pos, f = make(41, 4, 2, 8, 8, torch.bfloat16)
+    out = torch.full_like(x, 7.0)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        bi.bi_rope(x, pos, f, inverse=torch.ones(2, dtype=torch.bool), out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+    assert same_bits(bi.bi_rope(x, pos, f, inverse=torch.tensor(True)), bi.bi_rope(x, pos, f, inverse=True))
