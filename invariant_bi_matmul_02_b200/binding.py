@@ -443,6 +443,9 @@ def load_marshal():
         except ImportError as e:
             raise RuntimeError("the binding's extension module _marshal.so is missing or does not load: build it with "
                                "__graft_entry__.build() or invariant_bi_matmul_02_b200/csrc/build.py") from e
+        if not (m.__doc__ or "").endswith(f"built for torch {torch.__version__};"):
+            raise RuntimeError(f"the binding's extension module _marshal.so was not built for torch {torch.__version__}: "
+                               "build it with __graft_entry__.build() or invariant_bi_matmul_02_b200/csrc/build.py")
         m.bind(BiError, *[ctypes.cast(getattr(lib, n), _p).value for n in (
             "bi_rope", "bi_paged_append", "bi_paged_decode_attention", "bi_paged_decode_attention_scratch_bytes",
             "bi_token_logprobs")])

@@ -47,17 +47,27 @@ MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 
 
+def marshal_current() -> bool:
+    """Whether the extension module is there, newer than its sources and built against this torch."""
+    import torch
+    deps = [MARSHAL_SRC, os.path.join(INCLUDE, "bi.h")]
+    if not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < max(os.path.getmtime(p) for p in deps):
+        return False
+    with open(MARSHAL, "rb") as f:
+        return f"built for torch {torch.__version__};".encode() in f.read()
+
+
 def build_marshal(force: bool = False) -> str:
     """The binding's extension module (argument marshalling only; no kernels), against torch's headers."""
-    deps = [MARSHAL_SRC, os.path.join(INCLUDE, "bi.h")]
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= max(os.path.getmtime(p) for p in deps):
+    if not force and marshal_current():
         return MARSHAL
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f'-DBI_TORCH_VERSION="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-o", MARSHAL, MARSHAL_SRC,

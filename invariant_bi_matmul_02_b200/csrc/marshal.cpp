@@ -385,8 +385,16 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyMethodDef methods[] = {BI_METHOD(bind),         BI_METHOD(rope),
                          BI_METHOD(paged_append), BI_METHOD(paged_decode_attention),
                          BI_METHOD(token_logprobs), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of binding.py's decode-step operators.", -1, methods,
-                      nullptr,               nullptr,    nullptr,                                                         nullptr};
+// The docstring names the torch whose headers this was built with: binding.py loads it with no other.
+PyModuleDef module = {PyModuleDef_HEAD_INIT,
+                      "_marshal",
+                      "Argument marshalling of binding.py's decode-step operators, built for torch " BI_TORCH_VERSION ";",
+                      -1,
+                      methods,
+                      nullptr,
+                      nullptr,
+                      nullptr,
+                      nullptr};
 
 }  // namespace
 

@@ -194,3 +194,18 @@ def test_missing_extension_module_fails_loudly(monkeypatch):
     monkeypatch.delattr(sys.modules["invariant_bi_matmul_02_b200"], "_marshal", raising=False)
     with pytest.raises(RuntimeError, match="_marshal.so"):
         binding.load_marshal()
+
+
+def test_extension_module_of_another_torch(lib, monkeypatch):
+    """An extension module built for another torch is rebuilt, and refused where it is loaded."""
+    assert libbuild.marshal_current()
+    runs = []
+    monkeypatch.setattr(libbuild.subprocess, "run", lambda cmd, **kw: runs.append(cmd))
+    libbuild.build_marshal()
+    assert not runs
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    libbuild.build_marshal()
+    assert len(runs) == 1
+    monkeypatch.setattr(binding, "_marshal", None)
+    with pytest.raises(RuntimeError, match="0.0.1"):
+        binding.load_marshal()
