@@ -454,7 +454,8 @@ bi_status bi_token_logprobs(const void *x, int64_t ldx, bi_dtype x_dtype, const 
 /*
  * bi_get_device_status -- synchronise `stream`, then read and clear the current
  * device's status word.  *out receives BI_OK or the first error a kernel recorded
- * since the last read (BI_ERR_TIMEOUT for a bounded wait that ran out).
+ * since the last read (BI_ERR_TIMEOUT for a bounded wait that ran out, BI_ERR_INVALID_ARG for a length, page,
+ * place or token that a kernel found out of range).
  * Returns BI_ERR_CUDA if the synchronisation or the read fails.
  */
 bi_status bi_get_device_status(void *stream, int32_t *out);

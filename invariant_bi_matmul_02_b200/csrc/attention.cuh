@@ -95,7 +95,7 @@ __device__ __forceinline__ int64_t attn_len(const AttnParams &p, int b, bool rep
 {
     int64_t L = cached && b < kAttnLensCached ? cached[b] : p.lens[b];
     if (L < 1 || L > p.Lmax) {
-        if (report) *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+        if (report) record_error(p.status, 1);  // BI_ERR_INVALID_ARG
         L = L < 1 ? 1 : p.Lmax;
     }
     return L;
@@ -149,7 +149,7 @@ __device__ __forceinline__ bool wait_flag_at_least(volatile int *flag, int v, vo
             if (*flag >= v) return true;
         if (*abort_flag) return false;
         if (global_timer_ns() - t0 > limit_ns) {
-            *reinterpret_cast<volatile int32_t *>(status) = 5;  // BI_ERR_TIMEOUT
+            record_error(status, 5);  // BI_ERR_TIMEOUT
             *abort_flag = 1;
             return false;
         }

@@ -27,7 +27,7 @@
 #include "rowops.cuh"
 #include "token_logprobs.cuh"
 
-// Per-device status word: 0, or the first error a kernel recorded (BI_ERR_TIMEOUT).
+// Per-device status word: 0, or the first error a kernel recorded (BI_ERR_TIMEOUT or BI_ERR_INVALID_ARG).
 __device__ int32_t g_bi_status = 0;
 
 namespace {

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         int sum = 0;
         for (int j = 0; j < per && b0 + j < p.B; ++j) {
             const int given = p.lens[b0 + j], L = pg_len(given, p.max_len);
-            if (blockIdx.x == 0 && L != given) *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+            if (blockIdx.x == 0 && L != given) record_error(p.status, 1);  // BI_ERR_INVALID_ARG
             lens_s[b0 + j] = L;
             const int n = (int)pg_splits(L);
             sum += n > 0 ? n : 1;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 if (x >= 0 && x < cnt) {
                     int32_t pg = cur.page;
                     if (pg < 0 || pg >= p.pages) {  // no such page: recorded, and read as zeros (out of the map's range)
-                        *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                        record_error(p.status, 1);  // BI_ERR_INVALID_ARG
                         pg = p.pages;
                     }
                     uint8_t *dst = smem + stage * C::kStageBytes + x * p.box * 128;

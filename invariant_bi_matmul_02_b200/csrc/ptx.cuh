@@ -337,6 +337,9 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 namespace bi {
 
+// Record an error (a bi_status) in the device status word, unless an earlier one is there.
+__device__ __forceinline__ void record_error(int32_t *status, int32_t code) { atomicCAS(status, 0, code); }
+
 // Bounded wait on (bar, parity).  Returns false if the wait ran out (after recording
 // the timeout and raising the abort flag) or if another role already aborted.
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
@@ -351,7 +354,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
             if (mbar_try_wait(a, parity)) return true;
         if (*abort_flag) return false;
         if (global_timer_ns() - t0 > limit_ns) {
-            *reinterpret_cast<volatile int32_t *>(status) = 5;  // BI_ERR_TIMEOUT
+            record_error(status, 5);  // BI_ERR_TIMEOUT
             *abort_flag = 1;
             return false;
         }

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             // The angles do not need the page, which is still on its way.
             if (p.R > 0) rope_angles(cs, p.inv_freq, p.R / 2, p.positions ? p.positions[t] : (int32_t)w.at, p.scale, false);
             if (w.page < 0 || w.page >= p.pages)
-                *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                record_error(p.status, 1);  // BI_ERR_INVALID_ARG
             else
                 row = w.page * p.c_page + (w.at % p.page_size) * p.c_token;
         }

@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kTlThreads, kTlBlocks) token_logprobs_kernel(c
             if (p.logprobs != nullptr) {
                 float v = 0.0f;  // a negative token: the row is not scored
                 if (tok >= p.V) {
-                    *reinterpret_cast<volatile int32_t *>(p.status) = 1;  // BI_ERR_INVALID_ARG
+                    record_error(p.status, 1);  // BI_ERR_INVALID_ARG
                     v = __int_as_float(0x7fffffff);
                 } else if (tok >= 0) {
                     v = tl_logprob(tok_x, a.m, p.scale, log_s);

@@ -31,3 +31,32 @@ def test_wait_that_runs_out_reports_timeout_and_context_survives():
 def test_selftest_limit_is_validated():
     with pytest.raises(bi.BiError):
         bi.bi_selftest_wait_timeout(10)
+
+
+def bad_calls():
+    """Calls that each record BI_ERR_INVALID_ARG: a token, a length, a page and a place out of range."""
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    n = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, cache, table = z(1, 1, 64), z(2, 16, 1, 64), n(9).view(1, 1)
+    return {
+        "token": lambda: bi.bi_token_logprobs(z(1, 8), n(8)),
+        "length": lambda: bi.bi_decode_attention(q, z(1, 16, 1, 64), z(1, 16, 1, 64), n(17)),
+        "paged length": lambda: bi.bi_paged_decode_attention(q, cache, cache, n(0).view(1, 1), n(-1)),
+        "page": lambda: bi.bi_paged_decode_attention(q, cache, cache, table, n(5)),
+        "place": lambda: bi.bi_paged_append(q, q, cache, cache, table, n(5)),
+    }
+
+
+@pytest.mark.parametrize("kind", ["token", "length", "paged length", "page", "place"])
+def test_the_first_error_is_kept(kind):
+    bad = bad_calls()[kind]
+    assert bi.bi_get_device_status() == bi.BI_OK
+    bad()
+    assert bi.bi_get_device_status() == bi.BI_ERR_INVALID_ARG
+    bi.bi_selftest_wait_timeout(1_000_000)
+    bad()
+    assert bi.bi_get_device_status() == bi.BI_ERR_TIMEOUT
+    bad()
+    bi.bi_selftest_wait_timeout(1_000_000)
+    assert bi.bi_get_device_status() == bi.BI_ERR_INVALID_ARG
+    assert bi.bi_get_device_status() == bi.BI_OK
