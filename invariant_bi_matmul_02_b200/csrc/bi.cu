@@ -558,7 +558,7 @@ struct RopeLaunch {
     int shares, stages;
     dim3 grid;
     size_t smem;
-    RopeLaunch(int64_t T, int64_t steps, bool streamed, int R, int sms)
+    RopeLaunch(int64_t T, int64_t steps, bool streamed, int R, int sms, int resident = bi::kRopeBlocks)
     {
         steps = std::max<int64_t>(steps, 1);
         shares = rope_shares(T, steps, sms);
@@ -567,11 +567,13 @@ struct RopeLaunch {
         grid = dim3((unsigned)((T * shares + bi::kRopeWarps - 1) / bi::kRopeWarps));
         smem = (size_t)bi::kRopeWarps * (stages * 1024 + R * sizeof(float));
         // Launched while the kernel before it still holds places, a grid that fits the GPU at once would sit unevenly, up to
-        // kRopeBlocks on one SM and few on another.  A request for more shared memory than an SM has for one block above
-        // its share keeps the blocks apart (512 tokens appended 6.6 us without, 5.5 with; 3001 tokens of 13 heads of 96
-        // fp32 turned 7.6 and 7.1).  Fewer than four a SM would ask for more than 48 KB a block.
+        // `resident` blocks on one SM and few on another.  A request for more shared memory than an SM has for one block
+        // above its share keeps the blocks apart (512 tokens appended 6.6 us without, 5.5 with; 3001 tokens of 13 heads
+        // of 96 fp32 turned 7.6 and 7.1; staged, with up to kRopeStagedBlocks: 2048 tokens of 32 heads of 80, 20 turned,
+        // 6.8 and 5.6, 4000 of 19 of 192, 74 turned in place, 11.4 and 9.1).  Fewer than four a SM would ask for more than
+        // 48 KB a block.
         const int64_t per_sm = ((int64_t)grid.x + sms - 1) / sms;
-        if (per_sm >= 4 && per_sm < bi::kRopeBlocks)
+        if (per_sm >= 4 && per_sm < resident)
             smem = std::max<size_t>(smem, (size_t)(228 * 1024 / (per_sm + 1) - 1024 + 512));  // 1 KB a block is the system's
     }
 };
@@ -625,7 +627,8 @@ bi_status launch_append(const bi::AppendParams &p, bool half, int sms, cudaStrea
 bi_status launch_append_staged(const bi::AppendParams &p, bool half, int sms, cudaStream_t s)
 {
     const int64_t heads = 64 / p.pieces, Hq = p.q ? p.Hq : 0;
-    const RopeLaunch l(p.T, (Hq + heads - 1) / heads + 2 * ((p.Hkv + heads - 1) / heads), true, p.R, sms);
+    const RopeLaunch l(p.T, (Hq + heads - 1) / heads + 2 * ((p.Hkv + heads - 1) / heads), true, p.R, sms,
+                       bi::kRopeStagedBlocks);
     const dim3 block(bi::kRopeThreads);
     return half ? launch_pdl(bi::paged_append_kernel<8, true, true>, l.grid, block, l.smem, s, p, l.shares, l.stages)
                 : launch_pdl(bi::paged_append_kernel<8, false, true>, l.grid, block, l.smem, s, p, l.shares, l.stages);
@@ -1030,11 +1033,17 @@ bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, 
     p.copy_piece = x == y ? 0 : copy_piece(R, D - R, entry, strided);
     const bool half = layout == BI_ROPE_HALF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t W = 16 / entry, pieces = ((x == y ? R : D) + W - 1) / W;
-    if (R > 0 && !fits(W) && D % W == 0 && pieces <= 64 && strided(W)) {
+    const int64_t W = 16 / entry, pieces = ((x == y ? R : D) + W - 1) / W, narrow = fits(2) ? 2 : 1;
+    // Pairs that fill no 16-byte pieces are turned in shared memory, or walked through registers in narrower pieces.  The walk is
+    // the faster in place, where it moves the turned entries only, if the lanes take a head's pairs at once and the pieces
+    // are fp32 or the tokens few (us, staged and walked, in place: fp32, 2600 tokens of 16 heads, 60 turned 6.2 and 5.0, 132
+    // turned 14.8 and 14.2; bf16, 20 of 80 entries of 32 heads, 1 token 2.6 and 2.3, 8284 13.4 and 14.5).  Between two tensors
+    // staging is (the latter 8284: 18.2 and 24.0; fp32 29.3 and 35.8; 16 sizes of fp32 pairs 0.8 to 1.06 of the walk).
+    const bool walk = x == y && R / 2 <= 32 * narrow && (!bf16 || T < dev->sms);
+    if (R > 0 && !fits(W) && !walk && D % W == 0 && pieces <= 64 && strided(W)) {
         p.pieces = (int32_t)pieces;
         const int64_t heads = 64 / pieces;
-        const RopeLaunch l(T, (H + heads - 1) / heads, true, p.R, dev->sms);
+        const RopeLaunch l(T, (H + heads - 1) / heads, true, p.R, dev->sms, bi::kRopeStagedBlocks);
         return bf16 ? launch_rope_staged<__nv_bfloat16>(p, half, l, s) : launch_rope_staged<float>(p, half, l, s);
     }
     if (bf16)

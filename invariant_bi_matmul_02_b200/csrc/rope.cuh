@@ -31,6 +31,7 @@ namespace bi {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 7;  // resident per SM, a bound on registers (4096 x 40 x 128: 17.5 us with 6, 15.5 with 7)
+constexpr int kRopeStagedBlocks = 10;  // the same of the staged walk, as its 44 registers allow (9 for the append's 56)
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeMaxDim = 1024;  // head size limit: kRopeWarps * D/2 cosines and sines are 16 KB
 constexpr int kRopeCopies = 4;     // value pieces a lane has in flight
@@ -300,9 +301,9 @@ __device__ __forceinline__ bool rope_stream(const RopeStretch<E> (&st)[N], int t
 // The same for heads of 16-byte pieces that their pairs do not fill (R/2 is not a multiple of a piece's entries): the
 // first `pieces` pieces of a head (64 at most) are streamed as they lie, 64 / pieces heads to a step, and the pairs
 // turned in shared memory one by one, across the lanes, before the pieces go out.
-// (8284 tokens of 19 heads of 192 bf16 with 74 entries turned: 25.9 us, 46.5 when lanes read and wrote single entries; 9000
-// of 2 heads of 256, 254 turned: 9.9 and 17.5; 32 heads of 80, 20 turned: one token 2.4 and 2.9, 2048 6.7 and 6.1; 64
-// sequences' tokens appended with 32 query and 32 key and value heads of 80, 20 turned: 3.4 and 5.6.)
+// (8284 tokens of 19 heads of 192 bf16 with 74 entries turned: 26.8 us, 46.7 when lanes read and wrote single entries; of
+// 2 heads of 256, 254 turned: 9.5 and 15.9; 32 heads of 80, 20 turned: one token 2.4 and 2.7, 2048 5.6 and 6.2; 64
+// sequences' tokens appended with 32 query and 32 key and value heads of 80, 20 turned: 3.4 and 5.7.)
 template <typename E, bool HALF, int N, typename Ready, typename Dst>
 __device__ __forceinline__ bool rope_staged(const RopeStretch<E> (&st)[N], int turned, int R, int pieces, int share, int shares,
                                             uint4 *ring, int stages, const float *cs, Ready ready, Dst dst)

@@ -218,3 +218,20 @@ def test_rope_inverse_without_a_truth_value():
     torch.cuda.synchronize()
     assert bool((out == 7.0).all())
     assert same_bits(bi.bi_rope(x, pos, f, inverse=torch.tensor(True)), bi.bi_rope(x, pos, f, inverse=True))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D,R", [(32, 80, 20), (9, 192, 74), (3, 96, 36), (5, 64, 6), (4, 256, 250), (2, 192, 132)])
+def test_rope_staged_or_walked_gives_the_same_bits(H, D, R, dtype, layout):
+    """At every number of tokens where the choice, the warps that share a token or the blocks' spreading change: between two
+    tensors, in place, and without 16-byte alignment."""
+    for T in (1, 147, 148, 300, 700, 1800, 2048, 2300, 3600, 4300, 5000, 5400):
+        x, pos, f = make(T + D + R, T, H, D, R, dtype, start=300)
+        y = bi.bi_rope(x, pos, f, layout, 0.9)
+        check(y[-3:], x[-3:], pos[-3:], f, layout, 0.9, False)
+        off = torch.empty(T * H * D + 1, dtype=dtype, device=DEV)[1:].view(T, H, D)
+        off.copy_(x)
+        assert same_bits(bi.bi_rope(off, pos, f, layout, 0.9), y), T
+        assert bi.bi_rope(x, pos, f, layout, 0.9, out=x) is x
+        assert same_bits(x, y), T
