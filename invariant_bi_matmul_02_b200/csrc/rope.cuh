@@ -4,8 +4,8 @@
 // Entry pair (a, b) number i < R/2 of a head at position p becomes
 //   (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i],
 // times a scale; entries R .. D-1 are copied.  The angle is a product in fp64, reduced to a fraction
-// of a turn before it is rounded to fp32 (an fp32 angle of 10^6 radians would be off by 0.06), and
-// each output is one fp32 expression rounded once.  The work is elementwise, so every launch shape
+// of a turn before it is rounded to fp32 (an fp32 angle of 10^6 radians would be off by 0.06), what that rounding leaves
+// out is put back to first order, and each output is one fp32 expression rounded once.  The work is elementwise, so every launch shape
 // gives the same bits.
 //
 // Bound by memory for many tokens (B200: 40 heads of 128 of 8192 tokens, bf16, 28.9 us or 5.8 TB/s; 9734 tokens
@@ -68,8 +68,13 @@ __device__ __forceinline__ void from_f32(float v, __nv_bfloat16 &o) { o = __floa
 __device__ __forceinline__ void rope_angle(int32_t pos, double inv_freq, float scale, bool inverse, float &c, float &s)
 {
     const double turns = (double)pos * (inv_freq * 0.15915494309189533576888);
-    const float f = (float)(turns - rint(turns));  // in [-1/2, 1/2]
-    sincospif(2.0f * f, &s, &c);
+    const double part = turns - rint(turns);  // in [-1/2, 1/2]
+    const float f = (float)part, r = 6.2831853f * (float)(part - (double)f);
+    float c0, s0;
+    sincospif(2.0f * f, &s0, &c0);
+    // The angle that the rounding of f left out, at most 2^-23.3 radians: its square is below any bit.
+    c = __fmaf_rn(-r, s0, c0);
+    s = __fmaf_rn(r, c0, s0);
     if (inverse) s = -s;
     c = __fmul_rn(c, scale);
     s = __fmul_rn(s, scale);

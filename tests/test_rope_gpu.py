@@ -235,3 +235,22 @@ def test_rope_staged_or_walked_gives_the_same_bits(H, D, R, dtype, layout):
         assert same_bits(bi.bi_rope(off, pos, f, layout, 0.9), y), T
         assert bi.bi_rope(x, pos, f, layout, 0.9, out=x) is x
         assert same_bits(x, y), T
+
+
+@pytest.mark.parametrize("H", [1, 40])
+@pytest.mark.parametrize("T", [300, 60000])
+def test_rope_sines_and_cosines_to_an_ulp_and_a_half(T, H):
+    """Pairs (1, 0) and (0, 1) give the cosines and sines themselves: sincospif is within one unit of the last place (2^-24
+    below 1), what the angle's rounding to fp32 leaves out (up to 1.3 units) is put back with one rounding of half a
+    unit, and its square is below 2^-46."""
+    f = torch.tensor([1.0, 0.7310585786300049, 0.25, 0.0123456789, 1e-5, 3.0e-7, 0.5, 0.9], dtype=torch.float64, device=DEV)
+    pos = (torch.arange(T, device=DEV) * 7 - 300000).to(torch.int32)
+    angle = pos.double()[:, None] * f
+    for first in (True, False):
+        x = torch.zeros(T, H, 16, device=DEV)
+        x[..., :8 if first else 16] = 1.0
+        if not first:
+            x[..., :8] = 0.0
+        y = bi.bi_rope(x, pos, f).double()
+        for got, want in ((y[..., :8], angle.cos() if first else -angle.sin()), (y[..., 8:], angle.sin() if first else angle.cos())):
+            assert float((got - want[:, None]).abs().max()) <= 1.5 * 2.0 ** -24 + 2.0 ** -34
