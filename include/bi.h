@@ -332,7 +332,8 @@ bi_status bi_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, 
  *   BI_ROPE_YARN    {factor, original length, beta_fast, beta_slow}: frequency i is blended from f (more than
  *                   beta_fast turns within the original length) to f / factor (fewer than beta_slow) by a
  *                   linear ramp over i between the two bounds, floor and ceiling of
- *                   R log(length / (2 pi beta)) / (2 log theta).  scale 0.1 log(factor) + 1.
+ *                   R log(length / (2 pi beta)) / (2 log theta), the lower at least 0, the upper at most R - 1; with all
+ *                   pairs on one side of both, all are kept or all divided.  scale 0.1 log(factor) + 1.
  *   BI_ROPE_BANDED  {factor, original length, low, high}: wavelengths shorter than length / high keep f, longer than
  *                   length / low get f / factor, between them the two are blended linearly in
  *                   length / wavelength.  scale 1.

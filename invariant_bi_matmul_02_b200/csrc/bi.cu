@@ -1076,7 +1076,12 @@ bi_status bi_rope_freqs(int64_t R, double theta, bi_rope_kind kind, const double
         auto pair_of = [&](double turns) { return R * std::log(params[1] / (turns * kTwoPi)) / (2.0 * std::log(theta)); };
         low = std::fmax(std::floor(pair_of(params[2])), 0.0);
         high = std::fmin(std::ceil(pair_of(params[3])), (double)(R - 1));
-        if (low == high) high += 0.001;
+        if (high < 0.0) {  // every pair makes fewer than beta_slow turns
+            low = -2.0;
+            high = -1.0;
+        } else if (low >= high) {  // a step, or every pair makes more than beta_fast turns
+            high = low + 0.001;
+        }
     }
     for (int64_t i = 0; i < R / 2; ++i) {
         const double f = std::pow(theta, -2.0 * (double)i / (double)R);

@@ -158,6 +158,28 @@ def test_rope_freqs_formulas(lib):
     assert freqs(0, theta)[0] == []
 
 
+@pytest.mark.parametrize("R", [2, 64, 128])
+@pytest.mark.parametrize("theta", [1.0e4, 1.0e6])
+def test_yarn_keeps_fast_pairs_and_divides_slow_ones_whatever_the_length(lib, R, theta):
+    """Also where both bounds lie before the first pair or behind the last."""
+    fast, slow, factor = 32.0, 1.0, 4.0
+    base = [theta ** (-2.0 * i / R) for i in range(R // 2)]
+    at = lambda turns, L: R * math.log(L / (turns * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+    kept = divided = 0
+    for e in range(-40, 40):
+        L = 10.0 ** (e / 2)
+        got, _ = freqs(R, theta, "yarn", factor=factor, original_length=L)
+        for i, (f, g) in enumerate(zip(base, got)):
+            assert f / factor * (1 - 1e-14) <= g <= f * (1 + 1e-14)
+            if i <= at(fast, L) - 1:  # a whole pair clear of the bound, which is rounded to one
+                assert g == pytest.approx(f, rel=1e-14), (L, i)
+                kept += 1
+            if i >= at(slow, L) + 1:
+                assert g == pytest.approx(f / factor, rel=1e-14), (L, i)
+                divided += 1
+    assert kept and divided
+
+
 def test_rope_freqs_refusals(lib):
     for args, kw in [((3, 1e4), {}), ((-2, 1e4), {}), ((2048, 1e4), {}), ((64, 1.0), {}), ((64, math.inf), {}),
                      ((64, 1e4, "linear"), dict(factor=0.5)), ((64, 1e4, "linear"), dict(factor=math.nan)),
