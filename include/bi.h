@@ -312,8 +312,10 @@ size_t bi_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64
  *              and inv_freq may be NULL.
  *   layout     BI_ROPE_HALF: pair i is entries (i, i + R/2); BI_ROPE_INTERLEAVED: (2i, 2i + 1).
  *   The angle is an fp64 product reduced to a fraction of a turn, so far positions keep their
- *   digits; the rest is fp32 with one rounding to bf16.  16-byte pieces are moved where R/2, D - R,
- *   the strides and the addresses allow it, single entries otherwise, with the same bits.
+ *   digits; cosines and sines are within 1.5 * 2^-24 and the rest is fp32 with one rounding to bf16.  Heads move in
+ *   16-byte pieces where R/2, the strides and the addresses are multiples of them.  Where R/2 is not but D is, they move so
+ *   too and the pairs are turned in shared memory (fp32 heads and few tokens in place: as below).  Else pairs move two
+ *   entries or one at a time, and entries R .. D-1 in the widest pieces that fit them.  The bits are the same.
  *   T <= 2^31 - 1, H <= 65535.
  */
 typedef enum { BI_ROPE_HALF = 0, BI_ROPE_INTERLEAVED = 1 } bi_rope_layout;
@@ -383,7 +385,7 @@ typedef struct {
  * Two tokens must not share a place: pages that receive tokens belong to one sequence.  (Where two do, each
  * entry there is one of theirs, which one is not defined.)
  * D <= 1024, heads and Hq <= 65535, T, B < 2^31, pages and page_size <= 2^31 - 1.
- * Pieces as in bi_rope; k, v, q need no alignment beyond their type's.
+ * Pieces as in bi_rope between two tensors; k, v, q need no alignment beyond their type's.
  */
 bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
                           int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
@@ -402,8 +404,9 @@ bi_status bi_paged_append(const void *k, int64_t k_token_stride, int64_t k_head_
  *
  * Batch invariance: a sequence is one split up to 512 tokens and splits of 256 beyond, in tiles of 32, cuts
  * fixed by its own length; scores are fp32 dot products, four chains take a split's tiles w, w + 4, ... under
- * a running maximum and are folded in order, and splits in a tree fixed by their number.  A sequence's output does not depend on
- * the others, on where its pages lie, on the page size or on max_len.
+ * a running maximum and are folded in order, and splits in a tree fixed by their number.  The weights keep their fp32 bits.  A
+ * sequence's output does not depend on the others, on where its pages lie, on the page size or on max_len.  Keys and values
+ * of its own tokens should be finite (an infinite value gives NaN); what lies past its end may be anything.
  *
  *   q        device, bf16, [B, Hq, D], heads consecutive, sequences q_stride elements apart (a multiple of 8).
  *   out      device, bf16, [B, Hq, D] contiguous (one rounding).

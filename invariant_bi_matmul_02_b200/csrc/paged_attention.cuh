@@ -24,8 +24,9 @@
 // Tensor-core work (mma.sync m16n8k16, bf16 in, fp32 accumulate): S^T = K Q^T with tokens on the 16
 // rows and the group's heads on the 8 columns (two column tiles for groups of 9 to 16), then
 // O^T += V^T P^T with the head's entries on the rows.  An fp32 weight enters as three bf16 terms, its upper 8, next 8
-// and last 8 bits (pg_terms), whose sum it is, so the only rounding to fewer than 24 bits is the output's.  (With two
-// terms, 16 bits, one output in 500 rounded the other way.)
+// and last 8 bits (pg_terms), whose sum it is, so the only rounding to fewer than 24 bits is the output's.  (Two
+// terms, 16 bits, made one output in 500 round otherwise than in fp32.  The third costs nothing where memory bounds, 0.1 us of
+// one sequence's 5.7, 0.4 of the ragged batch's 25, and with 16 query heads per kv head 112 us for 105 at 32 x 4096.)
 #pragma once
 
 #include <cstdint>

@@ -14,7 +14,8 @@
 //
 // Many rows are bound by memory and by the issue slots (2.4 of 4 instructions a cycle, beside the special-function
 // unit's half): 1024 rows of 151936 bf16 take 53 us, 5.9 TB/s, and fp32 96 us, 6.5 TB/s; with the 5 best 59 and
-// 103.  One row is bound by latency: 5.1 us, 8.2 with the 20 best.
+// 103 (from a replayed graph; as one call among others 64.5).  One row is bound by latency: 5.1 us, 8.0 to 8.4 with the 20
+// best.
 //
 // The k best: only the groups' maxima are kept during the pass.  The k best elements lie in the k best groups (larger
 // maximum first, lower group first among equals, as groups are consecutive), so the end of the row reads a few
