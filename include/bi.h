@@ -314,8 +314,9 @@ size_t bi_decode_attention_scratch_bytes(int64_t B, int64_t Hq, int64_t D, int64
  *   The angle is an fp64 product reduced to a fraction of a turn, so far positions keep their
  *   digits; cosines and sines are within 1.5 * 2^-24 and the rest is fp32 with one rounding to bf16.  Heads move in
  *   16-byte pieces where R/2, the strides and the addresses are multiples of them.  Where R/2 is not but D is, they move so
- *   too and the pairs are turned in shared memory (fp32 heads and few tokens in place: as below).  Else pairs move two
- *   entries or one at a time, and entries R .. D-1 in the widest pieces that fit them.  The bits are the same.
+ *   too and the pairs are turned in shared memory, but for some calls in place, where the turned entries alone move.  Else
+ *   pairs move two entries or one at a time, and entries R .. D-1 in the widest pieces that fit them.  The bits are the
+ *   same.
  *   T <= 2^31 - 1, H <= 65535.
  */
 typedef enum { BI_ROPE_HALF = 0, BI_ROPE_INTERLEAVED = 1 } bi_rope_layout;

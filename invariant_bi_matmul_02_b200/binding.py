@@ -175,7 +175,8 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     if isinstance(stream, torch.cuda.Stream):
         _same_device(stream.device.index, "stream")
     else:
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        handle = int(stream)  # 0 and 1 (cudaStreamLegacy) name the default stream
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

@@ -129,7 +129,8 @@ struct CallStream {
         }
         raw = PyLong_AsVoidPtr(o);
         if (!raw && PyErr_Occurred()) throw python_error();
-        guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), (c10::DeviceIndex)dev));
+        const cudaStream_t s = static_cast<cudaStream_t>(raw);  // cudaStreamLegacy is another handle of the default stream
+        guard.reset_stream(c10::cuda::getStreamFromExternal(s == cudaStreamLegacy ? nullptr : s, (c10::DeviceIndex)dev));
     }
 };
 

@@ -70,7 +70,7 @@ def check_outputs(call):
     torch.cuda.synchronize()
     want = call(None)
     default = torch.cuda.default_stream()
-    for s, of in ((side, side), (side.cuda_stream, side), (None, default), (0, default)):
+    for s, of in ((side, side), (side.cuda_stream, side), (None, default), (0, default), (1, default)):
         got = call(s)
         torch.cuda.synchronize()
         for a, b in zip(got, want):
